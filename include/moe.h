@@ -84,8 +84,9 @@ typedef enum {
   MOE_E_FLAGS = 10,     /* unknown bit in moe_shape.flags                      */
   MOE_E_NONFINITE = 11, /* MOE_F_CHECK_FINITE found a NaN or infinity; caller
                            outputs were not written                            */
-  MOE_E_MEMORY = 12     /* a source buffer is not memory the device can read
+  MOE_E_MEMORY = 12,    /* a source buffer is not memory the device can read
                            (e.g. pageable host memory)                         */
+  MOE_E_VALUE = 13      /* a scalar parameter is not finite or out of range    */
 } moe_status;
 
 typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
@@ -405,6 +406,147 @@ int moe_stage_experts(const moe_shape* shape, const moe_experts* src, const moe_
 size_t moe_route_locality_blocks(int32_t T);
 int moe_route_locality(const moe_shape* shape, const int32_t* topk_ids, int32_t* overlap_prev,
                        int32_t* block_unique, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The path around the routed experts: the norms before and after a block,
+ * token rows in expert order for products computed elsewhere, and gradients.
+ * ------------------------------------------------------------------------
+ * The conventions above hold (device pointers, 16-byte aligned, densely
+ * packed, outputs disjoint from inputs and from each other, everything
+ * validated before anything is enqueued, nothing allocated or kept).  Sums,
+ * norm statistics and gradients are accumulated in float32 in an order that
+ * depends on the shape only, so results repeat bit for bit; every output is
+ * rounded once, from float32.  T == 0 is a no-op, except that the weight
+ * gradients dw [H] of the norms are then written as zeros.
+ *
+ * Norms.  For a row v of H features
+ *   norm(v, w)[h] = v[h] * rs(v) * (w[h] + weight_offset),
+ *   rs(v) = 1 / sqrt(mean_h v[h]^2 + eps).
+ * The sum of squares is a float32: rows past 1.8e19 in magnitude overflow it
+ * (rs = 0), as an infinity in the row does.  A NaN or infinity stays in its
+ * row (and in the columns of dw).
+ * Domain: 0 <= T <= 131072, 1 <= H <= 65536 (any H, odd ones too); act
+ * MOE_DT_F32 or MOE_DT_BF16; eps in [2^-126, 2^127], weight_offset and the
+ * scales finite (MOE_E_VALUE otherwise). */
+#define MOE_N_GATE_TOKEN 0x1u   /* gate: float32 [T], one factor per token        */
+#define MOE_N_GATE_FULL 0x2u    /* gate: act [T][H], one factor per element       */
+#define MOE_N_GATE_SIGMOID 0x4u /* the factor is sigmoid(gate) instead of gate    */
+#define MOE_N_NO_NORM 0x8u      /* moe_norm_out: no norm after the block (w NULL) */
+
+typedef struct {
+  int32_t T;             /* rows (tokens)                                   */
+  int32_t H;             /* features per row                                */
+  int32_t act;           /* moe_dtype of every matrix and of w              */
+  uint32_t flags;        /* MOE_N_* bits                                    */
+  float eps;
+  float weight_offset;   /* 0, or 1 where weights are stored as w - 1       */
+  float residual_scale;  /* factor of the residual path                     */
+  float branch_scale;    /* factor of the block's branch                    */
+} moe_norm;
+
+/* Bytes of workspace of the two norm gradients for this descriptor (partial
+ * column sums of dw).  Host-only, pure.  0 for an invalid descriptor or
+ * T == 0. */
+size_t moe_norm_workspace_size(const moe_norm* norm);
+
+/* The norm before a block: n[t] = norm(x[t], w).  x, n [T][H] act; w [H]
+ * act.  norm->flags must be 0 (MOE_E_FLAGS otherwise); the scales are not
+ * used. */
+int moe_norm_in(const moe_norm* norm, const void* x, const void* w, void* n, hipStream_t stream);
+
+/* Gradient of moe_norm_in for the output gradient dn, added to the gradient
+ * dres that reaches x over the residual path:
+ *   dx[t] = residual_scale * dres[t] + rs (g - xh mean_h(g xh)),
+ *   dw[h] = sum_t dn[t][h] xh[t][h],   g = dn (w + weight_offset),
+ *   xh = x rs(x).
+ * dn, x, dx [T][H] act; dres [T][H] act or NULL (taken as 0); dw float [H]
+ * or NULL (not wanted; workspace may then be NULL).  rs is recomputed from
+ * x, so nothing is kept from the forward call. */
+int moe_norm_in_backward(const moe_norm* norm, const void* dn, const void* x, const void* w,
+                         const void* dres, void* dx, float* dw, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+
+/* The norm after a block, its gate, its residual scale, and the norm before
+ * the next block, in one pass:
+ *   b = norm(z, w)  (z itself with MOE_N_NO_NORM, w NULL),
+ *   G = gate or sigmoid(gate) (1 without a gate flag, gate NULL),
+ *   v = residual_scale * residual + branch_scale * G * b,
+ *   out = round(v),  n_next = norm(v, w_next)  (of v before its rounding).
+ * z, out, n_next [T][H] act; w, w_next [H] act; gate as the flags say;
+ * residual [T][H] act or NULL (taken as 0); w_next and n_next both or
+ * neither (MOE_E_NULL otherwise). */
+int moe_norm_out(const moe_norm* norm, const void* z, const void* w, const void* gate,
+                 const void* residual, const void* w_next, void* out, void* n_next,
+                 hipStream_t stream);
+
+/* Gradient of moe_norm_out for the gradient dout of v (where n_next was
+ * used, dout is moe_norm_in_backward's dx for x = out, w = w_next, dn =
+ * the gradient of n_next, dres = the gradient of out, residual_scale = 1):
+ *   db = branch_scale dout,  g = G db (w + weight_offset),  zh = z rs(z),
+ *   dz = rs (g - zh mean_h(g zh))   (G db with MOE_N_NO_NORM),
+ *   dw[h] = sum_t G db zh,
+ *   dgate = db b, summed over h for a token gate, times G (1 - G) for a
+ *   sigmoid.
+ * The residual's gradient is residual_scale * dout, which the next
+ * moe_norm_in_backward adds as its dres.  dout, z, dz [T][H] act; dgate as
+ * gate, or NULL; dw float [H] or NULL.  Gate, weight and their gradients
+ * must match the flags (MOE_E_FLAGS: given without the flag; MOE_E_NULL:
+ * flag without the gate). */
+int moe_norm_out_backward(const moe_norm* norm, const void* dout, const void* z, const void* w,
+                          const void* gate, void* dz, void* dgate, float* dw, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
+/* moe_combine and moe_norm_out in one launch, for the token rows of
+ * `shape`: z[t] = sum_{j ascending} topk_w[t][j] * y[pair_row[t*top_k+j]],
+ * kept in float32, then as moe_norm_out.  norm->T, H and act must equal the
+ * shape's (MOE_E_SHAPE, MOE_E_DTYPE otherwise).  y [P][H] act; pair_row,
+ * topk_w as moe_combine, except that a pair whose pair_row is outside
+ * [0, P) is dropped: it adds nothing.  z [T][H] act or NULL (output, the
+ * rounded branch, for the gradient); the rest as moe_norm_out. */
+int moe_combine_norm(const moe_shape* shape, const moe_norm* norm, const void* y,
+                     const int32_t* pair_row, const float* topk_w, const void* w,
+                     const void* gate, const void* residual, const void* w_next, void* z,
+                     void* out, void* n_next, hipStream_t stream);
+
+/* Token rows in expert order, for expert products computed elsewhere:
+ * rows[pair_row[p]] = x[p / top_k], times topk_w[p] when topk_w is not NULL
+ * (route weights on the experts' inputs).  x [T][H] act; rows [P][H] act;
+ * pair_row [P] as from moe_permute; a pair whose pair_row is outside [0, P)
+ * is dropped, and rows that no pair names are left as they were.  Two pairs
+ * with the same row leave that row unspecified. */
+int moe_dispatch(const moe_shape* shape, const void* x, const int32_t* pair_row,
+                 const float* topk_w, void* rows, hipStream_t stream);
+
+/* Gradient of moe_dispatch for the gradient drows of its rows:
+ *   dx[t] = dx_in[t] + sum_{j ascending} topk_w[p] drows[pair_row[p]]
+ *   (weights 1 when topk_w is NULL),
+ *   dw[p] = sum_h drows[pair_row[p]][h] x[t][h]  (0 for a dropped pair).
+ * dx_in [T][H] act or NULL (another gradient of x, added); dw float
+ * [T][top_k] or NULL; dw needs topk_w and x (MOE_E_NULL otherwise); x may be
+ * NULL when dw is. */
+int moe_dispatch_backward(const moe_shape* shape, const void* drows, const int32_t* pair_row,
+                          const float* topk_w, const void* x, const void* dx_in, void* dx,
+                          float* dw, hipStream_t stream);
+
+/* Gradient of moe_combine for the gradient dout of its output:
+ *   dy[pair_row[p]] = topk_w[p] dout[p / top_k],
+ *   dw[p] = sum_h dout[p / top_k][h] y[pair_row[p]][h].
+ * (The residual's gradient is dout.)  dout [T][H] act; y, dy [P][H] act; dw
+ * float [T][top_k] or NULL; y may be NULL when dw is.  Dropped pairs (a
+ * pair_row outside [0, P)) get dw = 0; rows of dy that no pair names are
+ * left as they were. */
+int moe_combine_backward(const moe_shape* shape, const void* dout, const void* y,
+                         const int32_t* pair_row, const float* topk_w, void* dy, float* dw,
+                         hipStream_t stream);
+
+/* Gradient of moe_route's weights: dlogits[t][topk_ids[t][j]] =
+ * w_j (dw_j - sum_i w_i dw_i) with w = topk_w[t], dw the gradient of
+ * topk_w, and 0 for the experts that were not selected (the selection itself
+ * has no gradient).  topk_w, dw float [T][top_k]; topk_ids int32 [T][top_k],
+ * the entries of a token distinct (an entry outside [0, E) is left out of
+ * dlogits); dlogits float [T][E]. */
+int moe_route_backward(const moe_shape* shape, const int32_t* topk_ids, const float* topk_w,
+                       const float* dw, float* dlogits, hipStream_t stream);
 
 /* Measurement helper, not part of the layer: streams `bytes` (a non-zero
  * multiple of 16) from `buf` once with 16-byte loads spread over 2048

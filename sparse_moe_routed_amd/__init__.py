@@ -12,5 +12,9 @@ from ._abi import (  # noqa: F401
     moe_layer_noalloc, MOE_NOALLOC_SCRATCH_BYTES, moe_perm, moe_permute, moe_route,
     moe_route_locality, moe_route_locality_blocks, moe_shape, moe_stage_experts, moe_status_str,
     moe_stream_read, moe_tile_experts, moe_workspace_size,
+    MOE_N_GATE_FULL, MOE_N_GATE_SIGMOID, MOE_N_GATE_TOKEN, MOE_N_NO_NORM, make_norm,
+    moe_combine_backward, moe_combine_norm, moe_dispatch, moe_dispatch_backward, moe_norm,
+    moe_norm_in, moe_norm_in_backward, moe_norm_out, moe_norm_out_backward,
+    moe_norm_workspace_size, moe_route_backward,
 )
 from .layer import MoELayerBuffers  # noqa: F401

@@ -23,18 +23,25 @@ STATUS = {
     0: "MOE_OK", 1: "MOE_E_NULL", 2: "MOE_E_SHAPE", 3: "MOE_E_DTYPE", 4: "MOE_E_FORMAT",
     5: "MOE_E_ALIGN", 6: "MOE_E_ALIAS", 7: "MOE_E_WORKSPACE", 8: "MOE_E_LIMIT",
     9: "MOE_E_DEVICE", 10: "MOE_E_FLAGS", 11: "MOE_E_NONFINITE", 12: "MOE_E_MEMORY",
+    13: "MOE_E_VALUE",
 }
 EXPORTS = ("moe_workspace_size", "moe_status_str", "moe_tile_experts", "moe_route", "moe_permute",
            "moe_grouped_ffn", "moe_ffn_gate_up", "moe_ffn_down", "moe_ffn_fused",
            "moe_ffn_fused_items", "moe_device_clock_khz", "moe_combine", "moe_layer",
            "moe_stage_experts", "moe_route_locality_blocks", "moe_route_locality",
            "moe_stream_read", "moe_layer_noalloc", "moe_route_permute",
-           "moe_ffn_down_combine")
+           "moe_ffn_down_combine", "moe_norm_workspace_size", "moe_norm_in", "moe_norm_in_backward",
+           "moe_norm_out", "moe_norm_out_backward", "moe_combine_norm", "moe_dispatch",
+           "moe_dispatch_backward", "moe_combine_backward", "moe_route_backward")
 MOE_F_TILED_WEIGHTS = 0x1
 MOE_F_CHECK_FINITE = 0x2
 MOE_F_FUSED_FFN = 0x4
 MOE_STAGE_GATE_UP = 0x1
 MOE_STAGE_DOWN = 0x2
+MOE_N_GATE_TOKEN = 0x1
+MOE_N_GATE_FULL = 0x2
+MOE_N_GATE_SIGMOID = 0x4
+MOE_N_NO_NORM = 0x8
 
 
 class MoEError(RuntimeError):
@@ -59,6 +66,13 @@ class moe_perm(ctypes.Structure):
     _fields_ = [("counts", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
                 ("sorted_pair", ctypes.c_void_p), ("pair_row", ctypes.c_void_p),
                 ("active", ctypes.c_void_p), ("n_active", ctypes.c_void_p)]
+
+
+class moe_norm(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float)]
 
 
 _lib = None
@@ -103,6 +117,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_route_permute.argtypes = [P(moe_shape), vp, vp, vp, vp, vp, vp, P(moe_perm), vp, sz, vp]
     lib.moe_ffn_down_combine.argtypes = [P(moe_shape), vp, P(moe_experts), P(moe_perm), vp, vp, vp,
                                          vp, sz, vp]
+    lib.moe_norm_workspace_size.argtypes = [P(moe_norm)]
+    lib.moe_norm_workspace_size.restype = sz
+    lib.moe_norm_in.argtypes = [P(moe_norm), vp, vp, vp, vp]
+    lib.moe_norm_in_backward.argtypes = [P(moe_norm)] + [vp] * 7 + [sz, vp]
+    lib.moe_norm_out.argtypes = [P(moe_norm)] + [vp] * 8
+    lib.moe_norm_out_backward.argtypes = [P(moe_norm)] + [vp] * 8 + [sz, vp]
+    lib.moe_combine_norm.argtypes = [P(moe_shape), P(moe_norm)] + [vp] * 11
+    lib.moe_dispatch.argtypes = [P(moe_shape)] + [vp] * 5
+    lib.moe_dispatch_backward.argtypes = [P(moe_shape)] + [vp] * 8
+    lib.moe_combine_backward.argtypes = [P(moe_shape)] + [vp] * 7
+    lib.moe_route_backward.argtypes = [P(moe_shape)] + [vp] * 5
+    for name in ("moe_norm_in", "moe_norm_in_backward", "moe_norm_out", "moe_norm_out_backward",
+                 "moe_combine_norm", "moe_dispatch", "moe_dispatch_backward",
+                 "moe_combine_backward", "moe_route_backward"):
+        getattr(lib, name).restype = i32
     for name in ("moe_tile_experts", "moe_route", "moe_permute", "moe_grouped_ffn", "moe_ffn_gate_up",
                  "moe_ffn_down", "moe_ffn_fused", "moe_device_clock_khz", "moe_combine", "moe_layer",
                  "moe_route_locality", "moe_stage_experts", "moe_stream_read", "moe_layer_noalloc", "moe_route_permute",
@@ -293,3 +322,177 @@ def moe_stage_experts(shape, src, dst, perm, parts=None, stream=None, check=True
                                   None if perm is None else ctypes.byref(perm), parts,
                                   stream_handle(stream))
     return _ret(st, "moe_stage_experts", check)
+
+
+# ---------------------------------------------------------------------------
+# The path around the routed experts.  Tensors given to these calls are also
+# checked here for what a bare pointer cannot tell: type (MOE_E_DTYPE), size
+# and dense layout (MOE_E_SHAPE), memory of the current device (MOE_E_MEMORY).
+# ---------------------------------------------------------------------------
+
+
+def make_norm(T, H, act="bf16", eps=1e-6, weight_offset=0.0, residual_scale=1.0,
+              branch_scale=1.0, flags=0) -> moe_norm:
+    return moe_norm(T, H, ACT.get(act, act), flags, eps, weight_offset, residual_scale,
+                    branch_scale)
+
+
+_TORCH = None
+
+
+def _torch_types():
+    """(act dtypes by moe_dtype, float32, int32, current device index function)"""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = ((torch.float32, torch.bfloat16), torch.float32, torch.int32,
+                  torch.cuda.current_device)
+    return _TORCH
+
+
+def _check_tensors(stream, args) -> int:
+    """Status of (tensor, dtype, elements) triples; addresses and None pass."""
+    device, memory = None, 0
+    for t, dtype, n in args:
+        if t is None or isinstance(t, int):
+            continue
+        if t.dtype is not dtype:
+            return 3
+        if t.numel() != n or not t.is_contiguous():
+            return 2
+        if not t.is_cuda:
+            memory = 12
+            continue
+        if device is None:
+            device = _torch_types()[3]()
+            if stream is not None and not isinstance(stream, int) and stream.device_index != device:
+                memory = 12
+        if t.get_device() != device:
+            memory = 12
+    return memory
+
+
+def _act_type(act):
+    """The torch type of a moe_dtype (None, which no tensor has, for an
+    unknown one: the library reports that)."""
+    types = _torch_types()[0]
+    return types[act] if 0 <= act < len(types) else None
+
+
+def _workspace_status(workspace, nbytes) -> int:
+    """A workspace tensor must hold nbytes on the current device."""
+    if workspace is None or isinstance(workspace, int):
+        return 0
+    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
+        return 7
+    if not workspace.is_cuda or workspace.get_device() != _torch_types()[3]():
+        return 12
+    return 0
+
+
+def _gate_triple(norm, gate):
+    if norm.flags & MOE_N_GATE_TOKEN:
+        return gate, _torch_types()[1], norm.T
+    return gate, _act_type(norm.act), norm.T * norm.H
+
+
+def moe_norm_workspace_size(norm) -> int:
+    return int(load().moe_norm_workspace_size(ctypes.byref(norm)))
+
+
+def moe_norm_in(norm, x, w, n, stream=None, check=True) -> int:
+    a, m = _act_type(norm.act), norm.T * norm.H
+    st = _check_tensors(stream, ((x, a, m), (w, a, norm.H), (n, a, m)))
+    st = st or load().moe_norm_in(ctypes.byref(norm), ptr(x), ptr(w), ptr(n), stream_handle(stream))
+    return _ret(st, "moe_norm_in", check)
+
+
+def moe_norm_in_backward(norm, dn, x, w, dres, dx, dw, workspace, workspace_bytes, stream=None,
+                         check=True) -> int:
+    a, m, H = _act_type(norm.act), norm.T * norm.H, norm.H
+    st = _check_tensors(stream, ((dn, a, m), (x, a, m), (w, a, H), (dres, a, m), (dx, a, m),
+                                 (dw, _torch_types()[1], H)))
+    st = st or _workspace_status(workspace, workspace_bytes)
+    st = st or load().moe_norm_in_backward(ctypes.byref(norm), ptr(dn), ptr(x), ptr(w), ptr(dres),
+                                           ptr(dx), ptr(dw), ptr(workspace), workspace_bytes,
+                                           stream_handle(stream))
+    return _ret(st, "moe_norm_in_backward", check)
+
+
+def moe_norm_out(norm, z, w, gate, residual, w_next, out, n_next, stream=None, check=True) -> int:
+    a, m, H = _act_type(norm.act), norm.T * norm.H, norm.H
+    st = _check_tensors(stream, ((z, a, m), (w, a, H), _gate_triple(norm, gate), (residual, a, m),
+                                 (w_next, a, H), (out, a, m), (n_next, a, m)))
+    st = st or load().moe_norm_out(ctypes.byref(norm), ptr(z), ptr(w), ptr(gate), ptr(residual),
+                                   ptr(w_next), ptr(out), ptr(n_next), stream_handle(stream))
+    return _ret(st, "moe_norm_out", check)
+
+
+def moe_norm_out_backward(norm, dout, z, w, gate, dz, dgate, dw, workspace, workspace_bytes,
+                          stream=None, check=True) -> int:
+    a, m, H = _act_type(norm.act), norm.T * norm.H, norm.H
+    st = _check_tensors(stream, ((dout, a, m), (z, a, m), (w, a, H), _gate_triple(norm, gate),
+                                 (dz, a, m), _gate_triple(norm, dgate),
+                                 (dw, _torch_types()[1], H)))
+    st = st or _workspace_status(workspace, workspace_bytes)
+    st = st or load().moe_norm_out_backward(ctypes.byref(norm), ptr(dout), ptr(z), ptr(w),
+                                            ptr(gate), ptr(dz), ptr(dgate), ptr(dw),
+                                            ptr(workspace), workspace_bytes, stream_handle(stream))
+    return _ret(st, "moe_norm_out_backward", check)
+
+
+def moe_combine_norm(shape, norm, y, pair_row, topk_w, w, gate, residual, w_next, z, out, n_next,
+                     stream=None, check=True) -> int:
+    a, f32, i32 = _act_type(norm.act), _torch_types()[1], _torch_types()[2]
+    m, H, P = norm.T * norm.H, norm.H, shape.T * shape.top_k
+    st = _check_tensors(stream, ((y, a, P * shape.H), (pair_row, i32, P), (topk_w, f32, P),
+                                 (w, a, H), _gate_triple(norm, gate), (residual, a, m),
+                                 (w_next, a, H), (z, a, m), (out, a, m), (n_next, a, m)))
+    st = st or load().moe_combine_norm(ctypes.byref(shape), ctypes.byref(norm), ptr(y),
+                                       ptr(pair_row), ptr(topk_w), ptr(w), ptr(gate),
+                                       ptr(residual), ptr(w_next), ptr(z), ptr(out), ptr(n_next),
+                                       stream_handle(stream))
+    return _ret(st, "moe_combine_norm", check)
+
+
+def moe_dispatch(shape, x, pair_row, topk_w, rows, stream=None, check=True) -> int:
+    a, f32, i32 = _act_type(shape.act), _torch_types()[1], _torch_types()[2]
+    P = shape.T * shape.top_k
+    st = _check_tensors(stream, ((x, a, shape.T * shape.H), (pair_row, i32, P), (topk_w, f32, P),
+                                 (rows, a, P * shape.H)))
+    st = st or load().moe_dispatch(ctypes.byref(shape), ptr(x), ptr(pair_row), ptr(topk_w),
+                                   ptr(rows), stream_handle(stream))
+    return _ret(st, "moe_dispatch", check)
+
+
+def moe_dispatch_backward(shape, drows, pair_row, topk_w, x, dx_in, dx, dw, stream=None,
+                          check=True) -> int:
+    a, f32, i32 = _act_type(shape.act), _torch_types()[1], _torch_types()[2]
+    P, m = shape.T * shape.top_k, shape.T * shape.H
+    st = _check_tensors(stream, ((drows, a, P * shape.H), (pair_row, i32, P), (topk_w, f32, P),
+                                 (x, a, m), (dx_in, a, m), (dx, a, m), (dw, f32, P)))
+    st = st or load().moe_dispatch_backward(ctypes.byref(shape), ptr(drows), ptr(pair_row),
+                                            ptr(topk_w), ptr(x), ptr(dx_in), ptr(dx), ptr(dw),
+                                            stream_handle(stream))
+    return _ret(st, "moe_dispatch_backward", check)
+
+
+def moe_combine_backward(shape, dout, y, pair_row, topk_w, dy, dw, stream=None, check=True) -> int:
+    a, f32, i32 = _act_type(shape.act), _torch_types()[1], _torch_types()[2]
+    P = shape.T * shape.top_k
+    st = _check_tensors(stream, ((dout, a, shape.T * shape.H), (y, a, P * shape.H),
+                                 (pair_row, i32, P), (topk_w, f32, P), (dy, a, P * shape.H),
+                                 (dw, f32, P)))
+    st = st or load().moe_combine_backward(ctypes.byref(shape), ptr(dout), ptr(y), ptr(pair_row),
+                                           ptr(topk_w), ptr(dy), ptr(dw), stream_handle(stream))
+    return _ret(st, "moe_combine_backward", check)
+
+
+def moe_route_backward(shape, topk_ids, topk_w, dw, dlogits, stream=None, check=True) -> int:
+    f32, i32 = _torch_types()[1], _torch_types()[2]
+    P = shape.T * shape.top_k
+    st = _check_tensors(stream, ((topk_ids, i32, P), (topk_w, f32, P), (dw, f32, P),
+                                 (dlogits, f32, shape.T * shape.E)))
+    st = st or load().moe_route_backward(ctypes.byref(shape), ptr(topk_ids), ptr(topk_w), ptr(dw),
+                                         ptr(dlogits), stream_handle(stream))
+    return _ret(st, "moe_route_backward", check)

@@ -9,13 +9,10 @@
 #include <cstdint>
 #include <cstring>
 
+#include "abi_check.h"
 #include "moe_internal.h"
 
 namespace moe {
-
-static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-static size_t act_bytes(const moe_shape& s) { return s.act == MOE_DT_F32 ? 4 : 2; }
 
 static size_t wrow_bytes(const moe_shape& s, int K) {
   switch (s.wfmt) {
@@ -99,31 +96,7 @@ bool make_plan(const moe_shape& s, Plan* p) {
 // Validation helpers
 // ---------------------------------------------------------------------------
 
-struct Span {
-  const void* p;
-  size_t n;
-};
-
-static bool overlap(Span a, Span b) {
-  if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + b.n && b0 < a0 + a.n;
-}
-
-// Every output must be disjoint from every other output and every input.
-static bool any_alias(const Span* outs, int no, const Span* ins, int ni) {
-  for (int i = 0; i < no; ++i) {
-    for (int j = i + 1; j < no; ++j)
-      if (overlap(outs[i], outs[j])) return true;
-    for (int j = 0; j < ni; ++j)
-      if (overlap(outs[i], ins[j])) return true;
-  }
-  return false;
-}
-
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-static int check_shape(const moe_shape* s) {
+int check_shape(const moe_shape* s) {
   if (!s) return MOE_E_NULL;
   if (s->flags & ~(MOE_F_TILED_WEIGHTS | MOE_F_CHECK_FINITE | MOE_F_FUSED_FFN)) return MOE_E_FLAGS;
   if ((s->flags & MOE_F_FUSED_FFN) && !(s->flags & MOE_F_TILED_WEIGHTS)) return MOE_E_FLAGS;
@@ -146,16 +119,6 @@ static int check_shape(const moe_shape* s) {
   if ((s->flags & MOE_F_FUSED_FFN) && T * s->top_k > kFusedMaxPairs) return MOE_E_LIMIT;
   return MOE_OK;
 }
-
-static int check_ptrs(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (!p) return MOE_E_NULL;
-  for (const void* p : ps)
-    if (!aligned16(p)) return MOE_E_ALIGN;
-  return MOE_OK;
-}
-
-static int check_opt_ptr(const void* p) { return (p && !aligned16(p)) ? MOE_E_ALIGN : MOE_OK; }
 
 static int check_ws(const Plan& pl, void* ws, size_t bytes) {
   if (pl.total == 0) return MOE_OK;
@@ -222,8 +185,6 @@ static PermPtrs ws_perm(const moe_shape& s, const Plan& pl, void* ws) {
 static int32_t* ws_tiles(const Plan& pl, void* ws) {
   return reinterpret_cast<int32_t*>(static_cast<char*>(ws) + pl.tiles_off);
 }
-
-static int device_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_E_DEVICE; }
 
 // MOE_F_CHECK_FINITE: wait for the enqueued work and read the status word.
 static int finite_status(const Plan& pl, void* ws, hipStream_t st, hipError_t e) {
@@ -374,6 +335,7 @@ const char* moe_status_str(int status) {
     case MOE_E_FLAGS: return "MOE_E_FLAGS: unknown flag bit or unsupported flag combination";
     case MOE_E_NONFINITE: return "MOE_E_NONFINITE: NaN or infinity found; outputs not written";
     case MOE_E_MEMORY: return "MOE_E_MEMORY: a source buffer is not device-readable memory";
+    case MOE_E_VALUE: return "MOE_E_VALUE: scalar parameter not finite or out of range";
     default: return "unknown moe status";
   }
 }

@@ -49,6 +49,9 @@ struct Plan {
 
 bool make_plan(const moe_shape& s, Plan* p);
 
+// MOE_OK when the shape is in the domain of include/moe.h
+int check_shape(const moe_shape* s);
+
 // Supplies the workspace of a validated moe_layer call that received none:
 // `need` is the plan's size; on MOE_OK *ws / *ws_bytes describe device
 // memory of at least `need` bytes usable on `st`'s device.
@@ -134,6 +137,37 @@ hipError_t launch_zero_status(uint32_t* status, hipStream_t st);
 // sets `bit` in *status if any of the n values (bf16 or float32) is NaN/inf
 hipError_t launch_check_finite(const void* src, size_t n, bool bf16, uint32_t bit,
                                uint32_t* status, hipStream_t st);
+// The norms around the block.  Forward: z is a matrix, or (y, pair_row,
+// topk_w, k given) the combine of a token's slots; norm_in is the forward
+// kernel without gate, residual and next norm.
+struct NormFwd {
+  const void* z;
+  const void* y;
+  const int32_t* pair_row;
+  const float* topk_w;
+  int k;
+  const void *w, *gate, *residual, *w_next;
+  void *z_out, *out, *n_next;
+};
+struct NormBwd {
+  const void *dout, *z, *w, *gate, *dres;
+  void *dz, *dgate;
+  float *dw, *part;   // part: float [norm_bwd_groups][H]
+};
+int norm_bwd_groups(const moe_norm& n);   // workgroups of the gradient kernel
+hipError_t launch_norm_fwd(const moe_norm& n, const NormFwd& a, hipStream_t st);
+hipError_t launch_norm_bwd(const moe_norm& n, const NormBwd& a, hipStream_t st);
+// token rows in expert order and the gradients of dispatch, combine, route
+hipError_t launch_dispatch(const moe_shape& s, const void* x, const int32_t* pair_row,
+                           const float* w, void* rows, hipStream_t st);
+hipError_t launch_dispatch_bwd(const moe_shape& s, const void* drows, const int32_t* pair_row,
+                               const float* w, const void* x, const void* dx_in, void* dx,
+                               float* dw, hipStream_t st);
+hipError_t launch_combine_bwd(const moe_shape& s, const void* dout, const void* y,
+                              const int32_t* pair_row, const float* w, void* dy, float* dw,
+                              hipStream_t st);
+hipError_t launch_route_bwd(const moe_shape& s, const int32_t* ids, const float* w,
+                            const float* dw, float* dlogits, hipStream_t st);
 // pair_row == nullptr: y rows in pair order (row t*k + j)
 hipError_t launch_combine(const moe_shape& s, const void* y, const int32_t* pair_row,
                           const float* w, const void* residual, void* out, hipStream_t st);

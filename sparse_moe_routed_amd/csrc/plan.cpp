@@ -3,6 +3,7 @@
 // how many fused-FFN slices and route-locality values a shape has.  Plain
 // C++ with no device code, so the validation layer builds and runs without
 // a GPU.
+#include <algorithm>
 #include <cstddef>
 #include <cstdint>
 
@@ -47,6 +48,9 @@ bool tiles128_ok(const moe_shape& s) {
   return s.act == MOE_DT_BF16 && s.wfmt == MOE_WF_DENSE && (s.flags & MOE_F_TILED_WEIGHTS) &&
          s.I % 128 == 0;
 }
+
+// Workgroups of the norm gradient: each leaves one row of column sums.
+int norm_bwd_groups(const moe_norm& n) { return std::min(n.T, 512); }
 
 int locality_blocks(int T) {
   int n = 0;

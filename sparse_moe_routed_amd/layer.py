@@ -105,6 +105,48 @@ class MoELayerBuffers:
                                 self.topk_w if topk_w is None else topk_w, residual,
                                 self.out if out is None else out, stream)
 
+    def combine_norm(self, norm, w, gate=None, residual=None, w_next=None, z=None, out=None,
+                     n_next=None, y=None, stream=None):
+        """moe_combine_norm from this buffer's y, pair_row and topk_w into out
+        (default self.out) and n_next (with w_next)."""
+        return _abi.moe_combine_norm(self.shape, norm, self.y if y is None else y, self.pair_row,
+                                     self.topk_w, w, gate, residual, w_next, z,
+                                     self.out if out is None else out, n_next, stream)
+
+    def block(self, x, norm_in, w_in, w_router, bias, experts, norm_out, w_out, gate=None,
+              residual=None, w_next=None, n=None, out=None, n_next=None, stream=None):
+        """One block around the routed experts: norm before, route, grouped
+        FFN, then combine, norm after, gate, residual and the next block's
+        norm in one launch.  n [T][H] receives the normed rows, or holds them
+        already (the previous block's n_next) when norm_in is None."""
+        if norm_in is not None:
+            _abi.moe_norm_in(norm_in, x, w_in, n, stream)
+        self.route_permute(n, w_router, bias, logits=False, stream=stream)
+        self.ffn_gate_up(n, experts, stream=stream)
+        self.ffn_down(experts, stream=stream)
+        return self.combine_norm(norm_out, w_out, gate, residual, w_next, None, out, n_next,
+                                 stream=stream)
+
+    def dispatch(self, x, rows, weighted=False, stream=None):
+        """moe_dispatch of x into expert-ordered rows [T*k][H]; weighted: the
+        route weights multiply the rows."""
+        return _abi.moe_dispatch(self.shape, x, self.pair_row, self.topk_w if weighted else None,
+                                 rows, stream)
+
+    def dispatch_backward(self, drows, dx, dx_in=None, x=None, dw=None, weighted=False, stream=None):
+        """moe_dispatch_backward; dw (with x) for weighted rows."""
+        return _abi.moe_dispatch_backward(self.shape, drows, self.pair_row,
+                                          self.topk_w if weighted else None, x, dx_in, dx, dw, stream)
+
+    def combine_backward(self, dout, dy, dw=None, y=None, stream=None):
+        """moe_combine_backward with this buffer's y, pair_row and topk_w."""
+        return _abi.moe_combine_backward(self.shape, dout, self.y if y is None else y, self.pair_row,
+                                         self.topk_w, dy, dw, stream)
+
+    def route_backward(self, dw, dlogits, stream=None):
+        """moe_route_backward of this buffer's topk_ids and topk_w."""
+        return _abi.moe_route_backward(self.shape, self.topk_ids, self.topk_w, dw, dlogits, stream)
+
     def layer(self, x, w_router, bias, experts, residual=None, out=None, use_perm=True,
               stream=None):
         return _abi.moe_layer(self.shape, x, w_router, bias, experts, residual,
