@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void k_dispatch_bwd(const typename A::T* drows
     if (r >= 0 && r < P)
       for (int h = threadIdx.x; h < H; h += 256)
         s = fmaf(A::get(x[t * H + h]), A::get(drows[static_cast<size_t>(r) * H + h]), s);
-    s = row_sum<256>(s, red[j & 1]);
+    s = row_sum<false>(s, red[j & 1]);
     if (threadIdx.x == 0) dw[t * k + j] = s;
   }
 }
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(256) void k_combine_bwd(const typename A::T* dout,
         if (dw) s = fmaf(d, A::get(y[i]), s);
       }
     if (!dw) continue;
-    s = row_sum<256>(s, red[j & 1]);
+    s = row_sum<false>(s, red[j & 1]);
     if (threadIdx.x == 0) dw[t * k + j] = s;
   }
 }

@@ -1,7 +1,7 @@
-// The norms around a block: norm before it, and norm, gate, residual scale and
-// next norm after it, with their gradients (formulas: include/moe.h).
-//
-// One workgroup per row, element by element, every pass from memory.
+// The norms around a block, forward: the norm before it, and combine, norm,
+// gate, residual scale and next norm after it in one pass (formulas:
+// include/moe.h).  Bound by memory: every input is read once into registers,
+// every output written once, float32 in between.
 #include <algorithm>
 
 #include "moe_internal.h"
@@ -15,155 +15,185 @@ struct FwdArgs {
   int P;
 };
 
-// z[t][h] of the row: the matrix, or the combine of the token's slots
-template <class A, bool COMBINE>
-__device__ __forceinline__ float branch(const FwdArgs& p, size_t t, int h) {
+// Thread `tid` of the `nt` threads of a row holds chunks tid, tid + nt, ...
+// (C of them).  WAVE: a wave per row, blockDim / 64 rows per workgroup, no
+// barrier; else a workgroup per row.  An absent matrix is held as zeros
+// (weights: offset 1), so that nothing but loads depends on it.
+template <class A, bool WAVE, int C, bool COMBINE, bool ODD, int GATE>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
   typedef typename A::T E;
-  if constexpr (!COMBINE) return A::get(static_cast<const E*>(p.a.z)[t * p.n.H + h]);
-  float z = 0.f;
-  for (int j = 0; j < p.a.k; ++j) {
-    const int r = p.a.pair_row[t * p.a.k + j];
-    if (r < 0 || r >= p.P) continue;
-    z = fmaf(p.a.topk_w[t * p.a.k + j],
-             A::get(static_cast<const E*>(p.a.y)[static_cast<size_t>(r) * p.n.H + h]), z);
-  }
-  return z;
-}
-
-template <class A, bool COMBINE>
-__global__ __launch_bounds__(256) void k_norm_fwd(FwdArgs p) {
-  typedef typename A::T E;
-  __shared__ float red[2][4];
-  const size_t t = blockIdx.x;
+  constexpr int V = A::VEC;
+  __shared__ float red[WAVE ? 1 : 2][16];
+  const int nt = WAVE ? 64 : blockDim.x;
+  const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  const int t = WAVE ? __builtin_amdgcn_readfirstlane(blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6))
+                     : blockIdx.x;
+  if (t >= p.n.T) return;
   const int H = p.n.H;
-  const bool normed = !(p.n.flags & MOE_N_NO_NORM);
+  const size_t o = static_cast<size_t>(t) * H;
+  const uint32_t flags = p.n.flags;
+  const bool normed = !(flags & MOE_N_NO_NORM);
+  auto load = [&](const void* m, size_t at, int i) {
+    return load_chunk<A, ODD>(static_cast<const E*>(m) + at, i * nt + tid, H);
+  };
+  auto store = [&](void* m, int i, const float(&x)[V]) {
+    store_chunk<A, ODD>(static_cast<E*>(m) + o, i * nt + tid, H, x);
+  };
+
+  // everything is requested before the first use where registers allow
+  constexpr bool EARLY = C <= (WAVE ? 8 : 2);
+  constexpr u32x4_t zero = {0u, 0u, 0u, 0u};
+  auto weight = [&](int i) { return normed ? load(p.a.w, 0, i) : zero; };
+  auto gate = [&](int i) { return load(p.a.gate, o, i); };
+  auto residual = [&](int i) { return p.a.residual ? load(p.a.residual, o, i) : zero; };
+  u32x4_t wr[EARLY ? C : 1], gr[EARLY ? C : 1], rr[EARLY ? C : 1], nr[EARLY ? C : 1];
+  float v[C][V];
+  if constexpr (COMBINE) {
+    // slots in batches: the batch's rows are all requested, then added, j ascending
+    constexpr int KB = C == 1 ? 16 : C == 2 ? 8 : C == 4 ? 2 : 1;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[i][e] = 0.f;
+    const int32_t* pr = p.a.pair_row + static_cast<size_t>(t) * p.a.k;
+    const float* tw = p.a.topk_w + static_cast<size_t>(t) * p.a.k;
+    for (int j0 = 0; j0 < p.a.k; j0 += KB) {
+      u32x4_t y[KB][C];
+      float w[KB];
+#pragma unroll
+      for (int u = 0; u < KB; ++u) {
+        const int r = j0 + u < p.a.k ? pr[j0 + u] : -1;
+        const bool on = r >= 0 && r < p.P;
+        w[u] = on ? tw[j0 + u] : 0.f;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+          y[u][i] = on ? load(p.a.y, static_cast<size_t>(r) * H, i) : zero;
+      }
+#pragma unroll
+      for (int u = 0; u < KB; ++u)
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          float f[V];
+          A::unpack(y[u][i], f);
+#pragma unroll
+          for (int e = 0; e < V; ++e) v[i][e] = fmaf(w[u], f[e], v[i][e]);
+        }
+    }
+    if (p.a.z_out)
+#pragma unroll
+      for (int i = 0; i < C; ++i) store(p.a.z_out, i, v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) A::unpack(load(p.a.z, o, i), v[i]);
+  }
+  if constexpr (EARLY) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      wr[i] = weight(i);
+      if constexpr (GATE != kGateRow) gr[i] = gate(i);
+      rr[i] = residual(i);
+      if (p.a.n_next) nr[i] = load(p.a.w_next, 0, i);
+    }
+  }
+  float gt = 1.f;
+  if (flags & MOE_N_GATE_TOKEN) {
+    gt = static_cast<const float*>(p.a.gate)[t];
+    if (flags & MOE_N_GATE_SIGMOID) gt = sigmoid(gt);
+  }
   float rs = 1.f;
   if (normed) {
     float ss = 0.f;
-    for (int h = threadIdx.x; h < H; h += 256) {
-      const float z = branch<A, COMBINE>(p, t, h);
-      ss = fmaf(z, z, ss);
-    }
-    rs = rsqrtf(row_sum<256>(ss, red[0]) / H + p.n.eps);
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+    rs = rsqrtf(row_sum<WAVE>(ss, red[0]) / H + p.n.eps);
   }
-  auto value = [&](int h) {
-    float v = branch<A, COMBINE>(p, t, h);
-    if (normed) v = v * rs * (A::get(static_cast<const E*>(p.a.w)[h]) + p.n.weight_offset);
-    if (p.n.flags & (MOE_N_GATE_TOKEN | MOE_N_GATE_FULL)) {
-      float g = p.n.flags & MOE_N_GATE_TOKEN ? static_cast<const float*>(p.a.gate)[t]
-                                             : A::get(static_cast<const E*>(p.a.gate)[t * H + h]);
-      if (p.n.flags & MOE_N_GATE_SIGMOID) g = sigmoid(g);
-      v *= g;
-    }
-    v *= p.n.branch_scale;
-    if (p.a.residual)
-      v = fmaf(p.n.residual_scale, A::get(static_cast<const E*>(p.a.residual)[t * H + h]), v);
-    return v;
-  };
+  const float offset = normed ? p.n.weight_offset : 1.f, factor = gt * p.n.branch_scale;
   float ss = 0.f;
-  for (int h = threadIdx.x; h < H; h += 256) {
-    const float v = value(h);
-    static_cast<E*>(p.a.out)[t * H + h] = A::put(v);
-    if (p.a.z_out) static_cast<E*>(p.a.z_out)[t * H + h] = A::put(branch<A, COMBINE>(p, t, h));
-    ss = fmaf(v, v, ss);
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    if constexpr (!EARLY) asm volatile("" ::: "memory");   // keep the loads of a chunk together
+    float w[V], g[V], r[V];
+    A::unpack(EARLY ? wr[i] : weight(i), w);
+    A::unpack(EARLY ? rr[i] : residual(i), r);
+    if constexpr (GATE != kGateRow) A::unpack(EARLY ? gr[i] : gate(i), g);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      v[i][e] = v[i][e] * rs * (w[e] + offset) * factor;
+      if constexpr (GATE == kGateFull) v[i][e] *= g[e];
+      if constexpr (GATE == kGateFullSigmoid) v[i][e] *= sigmoid(g[e]);
+      v[i][e] = fmaf(p.n.residual_scale, r[e], v[i][e]);
+      ss = fmaf(v[i][e], v[i][e], ss);   // zeros past the row's end
+    }
+    store(p.a.out, i, v[i]);
   }
   if (!p.a.n_next) return;
-  const float rn = rsqrtf(row_sum<256>(ss, red[1]) / H + p.n.eps);
-  for (int h = threadIdx.x; h < H; h += 256)
-    static_cast<E*>(p.a.n_next)[t * H + h] =
-        A::put(value(h) * rn * (A::get(static_cast<const E*>(p.a.w_next)[h]) + p.n.weight_offset));
+  const float rn = rsqrtf(row_sum<WAVE>(ss, red[WAVE ? 0 : 1]) / H + p.n.eps);
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    float f[V];
+    A::unpack(EARLY ? nr[i] : load(p.a.w_next, 0, i), f);
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[i][e] *= rn * (f[e] + p.n.weight_offset);
+    store(p.a.n_next, i, v[i]);
+  }
+}
+
+typedef void (*FwdKernel)(FwdArgs);
+
+template <class A, bool ODD, int GATE>
+static FwdKernel fwd_wave(int C) {
+  switch (C) {
+    case 1: return k_norm_fwd<A, true, 1, false, ODD, GATE>;
+    case 2: return k_norm_fwd<A, true, 2, false, ODD, GATE>;
+    case 3: return k_norm_fwd<A, true, 3, false, ODD, GATE>;
+    case 4:
+    case 5: return k_norm_fwd<A, true, 5, false, ODD, GATE>;
+    default: return k_norm_fwd<A, true, 8, false, ODD, GATE>;
+  }
+}
+
+template <class A, bool COMBINE, bool ODD, int GATE>
+static FwdKernel fwd_block(int C) {
+  switch (C) {
+    case 1: return k_norm_fwd<A, false, 1, COMBINE, ODD, GATE>;
+    case 2: return k_norm_fwd<A, false, 2, COMBINE, ODD, GATE>;
+    case 4: return k_norm_fwd<A, false, 4, COMBINE, ODD, GATE>;
+    case 8: return k_norm_fwd<A, false, 8, COMBINE, ODD, GATE>;
+    default: return k_norm_fwd<A, false, 64 / A::VEC, COMBINE, ODD, GATE>;   // float32: 16
+  }
+}
+
+template <class A, bool COMBINE, int GATE>
+static hipError_t fwd(const FwdArgs& p, hipStream_t st) {
+  const int T = p.n.T, H = p.n.H, chunks = (H + A::VEC - 1) / A::VEC;
+  const bool odd = H % A::VEC != 0;   // never with COMBINE: H % 128 == 0 there
+  if (!COMBINE && chunks <= 8 * 64) {
+    const int C = (chunks + 63) / 64, rows = T >= 1024 ? 4 : 1;
+    auto kern = odd ? fwd_wave<A, true, GATE>(C) : fwd_wave<A, false, GATE>(C);
+    hipLaunchKernelGGL(kern, dim3((T + rows - 1) / rows), dim3(64 * rows), 0, st, p);
+  } else {
+    int C = 1;
+    while (chunks > 1024 * C) C *= 2;
+    const int nt = ((chunks + C - 1) / C + 63) / 64 * 64;
+    auto kern = odd ? fwd_block<A, COMBINE, !COMBINE, GATE>(C) : fwd_block<A, COMBINE, false, GATE>(C);
+    hipLaunchKernelGGL(kern, dim3(T), dim3(nt), 0, st, p);
+  }
+  return hipGetLastError();
+}
+
+template <class A, bool COMBINE>
+static hipError_t fwd_gate(const FwdArgs& p, hipStream_t st) {
+  if (!(p.n.flags & MOE_N_GATE_FULL)) return fwd<A, COMBINE, kGateRow>(p, st);
+  return p.n.flags & MOE_N_GATE_SIGMOID ? fwd<A, COMBINE, kGateFullSigmoid>(p, st)
+                                        : fwd<A, COMBINE, kGateFull>(p, st);
 }
 
 hipError_t launch_norm_fwd(const moe_norm& n, const NormFwd& a, hipStream_t st) {
   const FwdArgs p{a, n, n.T * a.k};
-  const bool bf = n.act == MOE_DT_BF16;
-  auto kern = a.y ? (bf ? k_norm_fwd<RowBf16, true> : k_norm_fwd<RowF32, true>)
-                  : (bf ? k_norm_fwd<RowBf16, false> : k_norm_fwd<RowF32, false>);
-  hipLaunchKernelGGL(kern, dim3(n.T), dim3(256), 0, st, p);
-  return hipGetLastError();
-}
-
-struct BwdArgs {
-  NormBwd a;
-  moe_norm n;
-};
-
-// Workgroup g takes rows g, g + G, ...; its column sums of dw stay in its row
-// of `part`, which only its own threads touch.
-template <class A>
-__global__ __launch_bounds__(256) void k_norm_bwd(BwdArgs p) {
-  typedef typename A::T E;
-  __shared__ float red[2][2][4];
-  const int H = p.n.H;
-  const bool normed = !(p.n.flags & MOE_N_NO_NORM);
-  const bool sig = p.n.flags & MOE_N_GATE_SIGMOID;
-  const E* dout = static_cast<const E*>(p.a.dout);
-  const E* z = static_cast<const E*>(p.a.z);
-  const E* w = static_cast<const E*>(p.a.w);
-  float* part = p.a.dw ? p.a.part + static_cast<size_t>(blockIdx.x) * H : nullptr;
-  int round = 0;
-  for (int t = blockIdx.x; t < p.n.T; t += gridDim.x, ++round) {
-    const size_t o = static_cast<size_t>(t) * H;
-    float gt = 1.f;
-    if (p.n.flags & MOE_N_GATE_TOKEN) {
-      gt = static_cast<const float*>(p.a.gate)[t];
-      if (sig) gt = sigmoid(gt);
-    }
-    auto gate = [&](int h) {
-      if (!(p.n.flags & MOE_N_GATE_FULL)) return gt;
-      const float g = A::get(static_cast<const E*>(p.a.gate)[o + h]);
-      return sig ? sigmoid(g) : g;
-    };
-    auto weight = [&](int h) { return normed ? A::get(w[h]) + p.n.weight_offset : 1.f; };
-    float ss = 0.f, s1 = 0.f;   // sum z^2, sum G db w z
-    for (int h = threadIdx.x; h < H; h += 256) {
-      const float zz = A::get(z[o + h]), d = p.n.branch_scale * A::get(dout[o + h]);
-      ss = fmaf(zz, zz, ss);
-      s1 = fmaf((p.n.flags & MOE_N_GATE_FULL ? gate(h) : 1.f) * d * weight(h), zz, s1);
-    }
-    ss = row_sum<256>(ss, red[round & 1][0]);
-    s1 = row_sum<256>(s1, red[round & 1][1]);
-    const float rs = normed ? rsqrtf(ss / H + p.n.eps) : 1.f;
-    if (p.n.flags & MOE_N_GATE_TOKEN) {
-      if (p.a.dgate && threadIdx.x == 0)
-        static_cast<float*>(p.a.dgate)[t] = rs * s1 * (sig ? gt * (1.f - gt) : 1.f);
-      s1 *= gt;
-    }
-    const float c = normed ? rs * s1 / H : 0.f;   // mean(g zh)
-    for (int h = threadIdx.x; h < H; h += 256) {
-      const float zh = A::get(z[o + h]) * rs, d = p.n.branch_scale * A::get(dout[o + h]);
-      const float G = gate(h), wh = weight(h);
-      float dz = G * d * wh;
-      if (normed) dz = rs * (dz - zh * c);
-      if (p.a.dres) dz = fmaf(p.n.residual_scale, A::get(static_cast<const E*>(p.a.dres)[o + h]), dz);
-      static_cast<E*>(p.a.dz)[o + h] = A::put(dz);
-      if (p.a.dgate && (p.n.flags & MOE_N_GATE_FULL))
-        static_cast<E*>(p.a.dgate)[o + h] = A::put(d * zh * wh * (sig ? G * (1.f - G) : 1.f));
-      if (part) part[h] = (round ? part[h] : 0.f) + G * d * zh;
-    }
-  }
-}
-
-__global__ __launch_bounds__(256) void k_norm_dw(const float* part, float* dw, int G, int H) {
-  const int h = blockIdx.x * 256 + threadIdx.x;
-  if (h >= H) return;
-  float s = 0.f;
-  for (int g = 0; g < G; ++g) s += part[static_cast<size_t>(g) * H + h];
-  dw[h] = s;
-}
-
-hipError_t launch_norm_bwd(const moe_norm& n, const NormBwd& a, hipStream_t st) {
-  const int G = norm_bwd_groups(n);
-  const BwdArgs p{a, n};
-  if (n.T > 0) {
-    auto kern = n.act == MOE_DT_BF16 ? k_norm_bwd<RowBf16> : k_norm_bwd<RowF32>;
-    hipLaunchKernelGGL(kern, dim3(G), dim3(256), 0, st, p);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (a.dw)
-    hipLaunchKernelGGL(k_norm_dw, dim3((n.H + 255) / 256), dim3(256), 0, st, a.part, a.dw, G, n.H);
-  return hipGetLastError();
+  if (n.act == MOE_DT_BF16) return a.y ? fwd_gate<RowBf16, true>(p, st) : fwd_gate<RowBf16, false>(p, st);
+  return a.y ? fwd_gate<RowF32, true>(p, st) : fwd_gate<RowF32, false>(p, st);
 }
 
 }  // namespace moe

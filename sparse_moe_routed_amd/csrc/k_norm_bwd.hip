@@ -1,0 +1,247 @@
+// Gradient of the norms around a block (formulas: include/moe.h).  One pass:
+// rs(z) and mean(g zh) come from two sums over the row, sum z^2 and
+// sum G d w z, taken together while the row is in registers; dz, the gate's
+// gradient and the row's share of dw follow from registers.  dw adds up in
+// float32 registers over the rows of a wave (or workgroup), then over the
+// waves of a workgroup in LDS, and a second launch adds the workgroups' rows
+// of partial sums: no atomics, the same bits every time.
+#include <algorithm>
+
+#include "moe_internal.h"
+#include "row_device.h"
+
+namespace moe {
+
+struct BwdArgs {
+  NormBwd a;
+  moe_norm n;
+};
+
+// WAVE: a wave per row, else a workgroup per row; rows t0, t0 + stride, ...
+// KEEP: the row stays in registers between the sums and the results
+// (otherwise it is read again, from the cache).  An absent matrix is held as
+// zeros (weights: offset 1), so that nothing but loads depends on it.
+template <class A, bool WAVE, int C, bool ODD, int GATE>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
+  typedef typename A::T E;
+  constexpr int V = A::VEC;
+  constexpr bool KEEP = WAVE || C <= 2;
+  __shared__ float2 red[2][WAVE ? 1 : 16];
+  extern __shared__ float colsum[];   // WAVE: [H], the workgroup's dw
+  const int nt = WAVE ? 64 : blockDim.x;
+  const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  const int wave = WAVE ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  const int waves = WAVE ? blockDim.x >> 6 : 1;
+  const int H = p.n.H;
+  const uint32_t flags = p.n.flags;
+  const bool normed = !(flags & MOE_N_NO_NORM), sig = flags & MOE_N_GATE_SIGMOID;
+  constexpr bool full = GATE != kGateRow;
+  const float bs = p.n.branch_scale;
+  auto load = [&](const void* m, size_t at, int i) {
+    return load_chunk<A, ODD>(static_cast<const E*>(m) + at, i * nt + tid, H);
+  };
+  float acc[C][V];
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[i][e] = 0.f;
+  constexpr u32x4_t zero = {0u, 0u, 0u, 0u};
+  const float offset = normed ? p.n.weight_offset : 1.f;
+  auto load_w = [&](int i) { return normed ? load(p.a.w, 0, i) : zero; };
+  auto load_s = [&](size_t o, int i) { return p.a.dres ? load(p.a.dres, o, i) : zero; };
+  u32x4_t wr[KEEP ? C : 1];
+  if constexpr (KEEP)
+#pragma unroll
+    for (int i = 0; i < C; ++i) wr[i] = load_w(i);
+  int parity = 0;
+  for (int t = blockIdx.x * waves + wave; t < p.n.T; t += gridDim.x * waves, parity ^= 1) {
+    const size_t o = static_cast<size_t>(t) * H;
+    u32x4_t zr[KEEP ? C : 1], dr[KEEP ? C : 1], gr[KEEP ? C : 1], sr[KEEP ? C : 1];
+    if constexpr (KEEP)
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        zr[i] = load(p.a.z, o, i);
+        dr[i] = load(p.a.dout, o, i);
+        if constexpr (full) gr[i] = load(p.a.gate, o, i);
+        sr[i] = load_s(o, i);
+      }
+    float gt = 1.f;
+    if (flags & MOE_N_GATE_TOKEN) {
+      gt = static_cast<const float*>(p.a.gate)[t];
+      if (sig) gt = sigmoid(gt);
+    }
+    auto gate = [&](int i, float(&g)[V]) {
+      if constexpr (full) A::unpack(KEEP ? gr[i] : load(p.a.gate, o, i), g);
+      if constexpr (GATE == kGateFullSigmoid)
+#pragma unroll
+        for (int e = 0; e < V; ++e) g[e] = sigmoid(g[e]);
+    };
+    float ss = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      if constexpr (!KEEP) asm volatile("" ::: "memory");   // keep the loads of a chunk together
+      float z[V], d[V], w[V], g[V];
+      A::unpack(KEEP ? zr[i] : load(p.a.z, o, i), z);
+      A::unpack(KEEP ? dr[i] : load(p.a.dout, o, i), d);
+      A::unpack(KEEP ? wr[i] : load_w(i), w);
+      gate(i, g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float dw = d[e] * (w[e] + offset);
+        ss = fmaf(z[e], z[e], ss);
+        s1 = fmaf(full ? g[e] * dw : dw, z[e], s1);
+      }
+    }
+    // the row is unpacked again after the sums: twice the registers would be
+    // live if its float32 values were kept
+    if constexpr (KEEP)
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        asm volatile("" : "+v"(zr[i]), "+v"(dr[i]), "+v"(wr[i]));
+        if constexpr (full) asm volatile("" : "+v"(gr[i]));
+      }
+    const float2 s = row_sum2<WAVE>(ss, s1, red[parity]);
+    const float rs = normed ? rsqrtf(s.x / H + p.n.eps) : 1.f;
+    s1 = bs * (rs * s.y);                                  // sum_h db zh (w) G_full
+    if ((flags & MOE_N_GATE_TOKEN) && p.a.dgate && tid == 0)
+      static_cast<float*>(p.a.dgate)[t] = s1 * (sig ? gt * (1.f - gt) : 1.f);
+    const float c = normed ? gt * s1 / H : 0.f;            // mean(g zh)
+    const float bg = bs * gt;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      if constexpr (!KEEP) asm volatile("" ::: "memory");
+      float z[V], d[V], w[V], g[V], r[V];
+      A::unpack(KEEP ? zr[i] : load(p.a.z, o, i), z);
+      A::unpack(KEEP ? dr[i] : load(p.a.dout, o, i), d);
+      A::unpack(KEEP ? wr[i] : load_w(i), w);
+      gate(i, g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        z[e] *= rs;
+        w[e] += offset;
+      }
+      if constexpr (full) {
+        if (p.a.dgate) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            r[e] = bs * d[e] * z[e] * w[e];
+            if constexpr (GATE == kGateFullSigmoid) r[e] *= g[e] * (1.f - g[e]);
+          }
+          store_chunk<A, ODD>(static_cast<E*>(p.a.dgate) + o, i * nt + tid, H, r);
+        }
+      }
+      float sv[V];
+      A::unpack(KEEP ? sr[i] : load_s(o, i), sv);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        d[e] *= full ? bg * g[e] : bg;
+        acc[i][e] = fmaf(d[e], z[e], acc[i][e]);
+        r[e] = rs * fmaf(-z[e], c, d[e] * w[e]);
+        r[e] = fmaf(p.n.residual_scale, sv[e], r[e]);
+      }
+      store_chunk<A, ODD>(static_cast<E*>(p.a.dz) + o, i * nt + tid, H, r);
+    }
+  }
+  if (!p.a.dw) return;
+  float* part = p.a.part + static_cast<size_t>(blockIdx.x) * H;
+  // WAVE: the waves add their sums in turn, the last one writes
+  for (int k = 0; k < waves; ++k) {
+    if (k == wave)
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const int h = (i * nt + tid) * V + e;
+          if (h < H) {
+            const float v = k == 0 ? acc[i][e] : colsum[h] + acc[i][e];
+            if (k == waves - 1)
+              part[h] = v;
+            else
+              colsum[h] = v;
+          }
+        }
+    if (k < waves - 1) __syncthreads();
+  }
+}
+
+// dw[h] = sum over G rows of part: 64 columns per workgroup, its 16 waves
+// take the rows in turn and add up in LDS, in wave order.
+__global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part,
+                                                  float* __restrict__ dw, int G, int H) {
+  __shared__ float sum[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int h = blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (h < H) {
+#pragma unroll 8
+    for (int g = wave; g < G; g += 16) s += part[static_cast<size_t>(g) * H + h];
+  }
+  sum[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && h < H) {
+    for (int i = 1; i < 16; ++i) s += sum[i][lane];
+    dw[h] = s;
+  }
+}
+
+typedef void (*BwdKernel)(BwdArgs);
+
+template <class A, bool ODD, int GATE>
+static BwdKernel bwd_kernel(bool wave, int C) {
+  if (wave) switch (C) {
+      case 1: return k_norm_bwd<A, true, 1, ODD, GATE>;
+      case 2: return k_norm_bwd<A, true, 2, ODD, GATE>;
+      case 3: return k_norm_bwd<A, true, 3, ODD, GATE>;
+      default: return k_norm_bwd<A, true, 5, ODD, GATE>;
+    }
+  switch (C) {
+    case 1: return k_norm_bwd<A, false, 1, ODD, GATE>;
+    case 2: return k_norm_bwd<A, false, 2, ODD, GATE>;
+    case 4: return k_norm_bwd<A, false, 4, ODD, GATE>;
+    case 8: return k_norm_bwd<A, false, 8, ODD, GATE>;
+    default: return k_norm_bwd<A, false, 64 / A::VEC, ODD, GATE>;   // float32: 16
+  }
+}
+
+template <class A, int GATE>
+static void bwd(const BwdArgs& p, int G, hipStream_t st) {
+  const int H = p.n.H, chunks = (H + A::VEC - 1) / A::VEC;
+  const bool wave = norm_bwd_wave(p.n);
+  int C = 1, nt = 64 * kNormWaves;
+  if (wave) {
+    C = (chunks + 63) / 64;
+  } else {
+    while (chunks > 1024 * C) C *= 2;
+    nt = ((chunks + C - 1) / C + 63) / 64 * 64;
+  }
+  auto kern = H % A::VEC ? bwd_kernel<A, true, GATE>(wave, C) : bwd_kernel<A, false, GATE>(wave, C);
+  hipLaunchKernelGGL(kern, dim3(G), dim3(nt), wave && p.a.dw ? H * sizeof(float) : 0, st, p);
+}
+
+template <class A>
+static void bwd_gate(const BwdArgs& p, int G, hipStream_t st) {
+  if (!(p.n.flags & MOE_N_GATE_FULL))
+    bwd<A, kGateRow>(p, G, st);
+  else if (p.n.flags & MOE_N_GATE_SIGMOID)
+    bwd<A, kGateFullSigmoid>(p, G, st);
+  else
+    bwd<A, kGateFull>(p, G, st);
+}
+
+hipError_t launch_norm_bwd(const moe_norm& n, const NormBwd& a, hipStream_t st) {
+  const int G = norm_bwd_groups(n);
+  const BwdArgs p{a, n};
+  if (n.T > 0) {
+    if (n.act == MOE_DT_BF16)
+      bwd_gate<RowBf16>(p, G, st);
+    else
+      bwd_gate<RowF32>(p, G, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.dw)
+    hipLaunchKernelGGL(k_norm_dw, dim3((n.H + 63) / 64), dim3(1024), 0, st, a.part, a.dw, G, n.H);
+  return hipGetLastError();
+}
+
+}  // namespace moe

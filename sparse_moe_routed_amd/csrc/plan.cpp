@@ -49,8 +49,18 @@ bool tiles128_ok(const moe_shape& s) {
          s.I % 128 == 0;
 }
 
+// In the gradient a wave holds rows of up to 320 16-byte chunks and their
+// column sums in registers; longer rows take a workgroup.
+bool norm_bwd_wave(const moe_norm& n) {
+  const int vec = n.act == MOE_DT_BF16 ? 8 : 4;
+  return n.H <= 320 * vec;
+}
+
 // Workgroups of the norm gradient: each leaves one row of column sums.
-int norm_bwd_groups(const moe_norm& n) { return std::min(n.T, 512); }
+int norm_bwd_groups(const moe_norm& n) {
+  const int rows = norm_bwd_wave(n) ? kNormWaves : 1;
+  return std::min((n.T + rows - 1) / rows, 512);
+}
 
 int locality_blocks(int T) {
   int n = 0;

@@ -54,23 +54,75 @@ struct RowF32 {
   }
 };
 
-// Sum of one value per thread over the NT threads of a row (NT = 64: one
-// wave; else the whole workgroup, through `slot`, NT / 64 floats of LDS that
-// no other reduction uses until the next barrier after this one).  Fixed
-// association, the result in every thread.
-template <int NT>
+// 16-byte chunk c of a row of H elements, zeros past its end.  ODD: H is no
+// multiple of VEC, so the last chunk is taken element by element.
+template <class A, bool ODD>
+__device__ __forceinline__ u32x4_t load_chunk(const typename A::T* row, int c, int H) {
+  constexpr int V = A::VEC;
+  if constexpr (!ODD) {
+    return c * V < H ? ld16(row + c * V) : u32x4_t{0u, 0u, 0u, 0u};
+  } else {
+    if ((c + 1) * V <= H) return *reinterpret_cast<const u32x4_e2*>(row + c * V);
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = c * V + i < H ? A::get(row[c * V + i]) : 0.f;
+    return A::pack(v);
+  }
+}
+
+template <class A, bool ODD>
+__device__ __forceinline__ void store_chunk(typename A::T* row, int c, int H,
+                                            const float (&v)[A::VEC]) {
+  constexpr int V = A::VEC;
+  if constexpr (!ODD) {
+    if (c * V < H) *reinterpret_cast<u32x4_t*>(row + c * V) = A::pack(v);
+  } else {
+    if ((c + 1) * V <= H) {
+      *reinterpret_cast<u32x4_e2*>(row + c * V) = A::pack(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (c * V + i < H) row[c * V + i] = A::put(v[i]);
+    }
+  }
+}
+
+// Sums of one or two values per thread over the threads of a row, in a fixed
+// association, the results in every thread.  WAVE: the row is one wave; else
+// it is the whole workgroup, and `slot` is one float (2) per wave in LDS that
+// no other reduction uses until the next barrier after this one.
+template <bool WAVE>
 __device__ __forceinline__ float row_sum(float v, float* slot) {
   v = wave_sum_f32(v);
-  if constexpr (NT > kWave) {
+  if constexpr (!WAVE) {
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
     __syncthreads();
     v = slot[0];
-#pragma unroll
-    for (int i = 1; i < NT / kWave; ++i) v += slot[i];
+    for (unsigned i = 1; i < blockDim.x >> 6; ++i) v += slot[i];
   }
   return v;
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+template <bool WAVE>
+__device__ __forceinline__ float2 row_sum2(float a, float b, float2* slot) {
+  float2 v = make_float2(wave_sum_f32(a), wave_sum_f32(b));
+  if constexpr (!WAVE) {
+    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = slot[0];
+    for (unsigned i = 1; i < blockDim.x >> 6; ++i) {
+      v.x += slot[i].x;
+      v.y += slot[i].y;
+    }
+  }
+  return v;
+}
+
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + expf(-g));
+}
+
+// Full gates of the norm kernels (a token gate is a factor of the whole row)
+constexpr int kGateRow = 0, kGateFull = 1, kGateFullSigmoid = 2;
 
 }  // namespace moe
