@@ -41,7 +41,7 @@ static size_t gate_bytes(const moe_norm& n) {
 }
 static size_t part_bytes(const moe_norm& n) {
   return n.T == 0 ? 0
-                  : align_up(static_cast<size_t>(norm_bwd_groups(n)) * n.H * sizeof(float), 256);
+                  : align_up(static_cast<size_t>(norm_bwd_groups(n)) * norm_part_pitch(n.H) * sizeof(float), 256);
 }
 
 // A pointer that must be given exactly when `flag` is set.

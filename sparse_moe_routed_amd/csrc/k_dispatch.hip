@@ -1,156 +1,250 @@
 // Token rows in expert order and the gradients of dispatch, combine and the
-// route weights (formulas: include/moe.h).
-//
-// One workgroup per token, element by element.
+// route weights (formulas: include/moe.h).  Bound by memory: every row is
+// read and written once, in 16-byte chunks, and the T tokens are the unit of
+// work, so that a token's own row is read once for its k slots.
+#include <algorithm>
+
 #include "moe_internal.h"
 #include "row_device.h"
 
 namespace moe {
 
+// One wave per 64 chunks of a token's row: the chunk stays in registers while
+// it is stored to each of the k rows.
 template <class A>
-__global__ __launch_bounds__(256) void k_dispatch(const typename A::T* x, const int32_t* pair_row,
-                                                  const float* w, typename A::T* rows, int H,
-                                                  int k, int P) {
-  const size_t t = blockIdx.x;
-  for (int j = 0; j < k; ++j) {
-    const int r = pair_row[t * k + j];
-    if (r < 0 || r >= P) continue;
-    for (int h = threadIdx.x; h < H; h += 256) {
-      const typename A::T v = x[t * H + h];
-      rows[static_cast<size_t>(r) * H + h] = w ? A::put(w[t * k + j] * A::get(v)) : v;
-    }
-  }
-}
-
-template <class A>
-__global__ __launch_bounds__(256) void k_dispatch_bwd(const typename A::T* drows,
-                                                      const int32_t* pair_row, const float* w,
-                                                      const typename A::T* x,
-                                                      const typename A::T* dx_in,
-                                                      typename A::T* dx, float* dw, int H, int k,
-                                                      int P) {
-  __shared__ float red[2][4];
-  const size_t t = blockIdx.x;
-  for (int h = threadIdx.x; h < H; h += 256) {
-    float s = 0.f;
-    for (int j = 0; j < k; ++j) {
-      const int r = pair_row[t * k + j];
-      if (r < 0 || r >= P) continue;
-      s = fmaf(w ? w[t * k + j] : 1.f, A::get(drows[static_cast<size_t>(r) * H + h]), s);
-    }
-    if (dx_in) s += A::get(dx_in[t * H + h]);
-    dx[t * H + h] = A::put(s);
-  }
-  if (!dw) return;
-  for (int j = 0; j < k; ++j) {
-    const int r = pair_row[t * k + j];
-    float s = 0.f;
-    if (r >= 0 && r < P)
-      for (int h = threadIdx.x; h < H; h += 256)
-        s = fmaf(A::get(x[t * H + h]), A::get(drows[static_cast<size_t>(r) * H + h]), s);
-    s = row_sum<false>(s, red[j & 1]);
-    if (threadIdx.x == 0) dw[t * k + j] = s;
-  }
-}
-
-template <class A>
-__global__ __launch_bounds__(256) void k_combine_bwd(const typename A::T* dout,
-                                                     const typename A::T* y,
-                                                     const int32_t* pair_row, const float* w,
-                                                     typename A::T* dy, float* dw, int H, int k,
-                                                     int P) {
-  __shared__ float red[2][4];
-  const size_t t = blockIdx.x;
-  for (int j = 0; j < k; ++j) {
-    const int r = pair_row[t * k + j];
-    const float wj = w[t * k + j];
-    float s = 0.f;
-    if (r >= 0 && r < P)
-      for (int h = threadIdx.x; h < H; h += 256) {
-        const float d = A::get(dout[t * H + h]);
-        const size_t i = static_cast<size_t>(r) * H + h;
-        dy[i] = A::put(wj * d);
-        if (dw) s = fmaf(d, A::get(y[i]), s);
+__global__ __launch_bounds__(256) void k_dispatch(const void* x, const int32_t* pair_row,
+                                                  const float* w, void* rows, int T, int H, int k,
+                                                  int P) {
+  constexpr int V = A::VEC;
+  const int parts = (H / V + 63) / 64;
+  const int unit = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  const int t = unit / parts, c = unit - t * parts;
+  if (t >= T) return;
+  const int lane = threadIdx.x & 63;
+  const u32x4_t v = RowRef<A, false>(x, static_cast<size_t>(t) * H, H).load(c, 64, lane);
+  const int32_t* pr = pair_row + static_cast<size_t>(t) * k;
+  for (int j0 = 0; j0 < k; j0 += 8) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int r = slot_row(pr, j0 + u, k, P);
+      if (r < 0) continue;
+      const RowRef<A, false> row(rows, static_cast<size_t>(r) * H, H);
+      if (w) {
+        const float wj = uniform_load(w + static_cast<size_t>(t) * k + j0 + u);
+        float f[V];
+        A::unpack(v, f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[e] *= wj;
+        row.store(c, 64, lane, f);
+      } else {
+        row.store_raw(c, 64, lane, v);
       }
-    if (!dw) continue;
-    s = row_sum<false>(s, red[j & 1]);
-    if (threadIdx.x == 0) dw[t * k + j] = s;
+    }
   }
 }
 
-// One wave per token; the row of dlogits is put together in LDS.
-__global__ __launch_bounds__(64) void k_route_bwd(const int32_t* ids, const float* w,
-                                                  const float* dw, float* dlogits, int E, int k) {
-  __shared__ float row[1024];
+// Slots whose rows are requested together: with top_k up to 16 a chunk's
+// sum is one round of loads.
+constexpr int kSlotBatch = 16;
+
+// dots[j * waves + wave]: a wave's share of slot j's dot product, over the
+// chunks of the row that it has seen (LDS; lane 0 of the wave keeps it).
+__device__ __forceinline__ void add_dot(float* dots, int j, float v, bool first) {
+  v = wave_sum_f32(v);
+  if ((threadIdx.x & 63) == 0) {
+    float* d = dots + j * (blockDim.x >> 6) + (threadIdx.x >> 6);
+    *d = first ? v : *d + v;
+  }
+}
+
+// dw[j]: the waves' shares in wave order.
+__device__ __forceinline__ void store_dots(const float* dots, float* dw, int k) {
+  const int waves = blockDim.x >> 6;
+  __syncthreads();
+  for (int j = threadIdx.x; j < k; j += blockDim.x) {
+    float s = dots[j * waves];
+    for (int i = 1; i < waves; ++i) s += dots[j * waves + i];
+    dw[j] = s;
+  }
+}
+
+// A workgroup per token: the sum over its slots' rows and, with DW, each
+// row's dot product with x.
+template <class A, bool DW>
+__global__ __launch_bounds__(1024) void k_dispatch_bwd(const void* drows, const int32_t* pair_row,
+                                                       const float* w, const void* x,
+                                                       const void* dx_in, void* dx, float* dw,
+                                                       int H, int k, int P) {
+  typedef RowRef<A, false> Row;
+  constexpr int V = A::VEC;
+  constexpr u32x4_t zero = {0u, 0u, 0u, 0u};
+  extern __shared__ float dots[];
+  const int nt = blockDim.x, tid = threadIdx.x;
   const size_t t = blockIdx.x;
-  float s = 0.f;
-  for (int j = threadIdx.x; j < k; j += 64) s = fmaf(w[t * k + j], dw[t * k + j], s);
-  s = wave_sum_f32(s);
-  for (int e = threadIdx.x; e < E; e += 64) row[e] = 0.f;
-  __syncthreads();
-  for (int j = threadIdx.x; j < k; j += 64) {
-    const int e = ids[t * k + j];
-    if (e >= 0 && e < E) row[e] = w[t * k + j] * (dw[t * k + j] - s);
+  for (int i = 0; i * nt * V < H; ++i) {
+    u32x4_t xr, ar;
+    if constexpr (DW) xr = Row(x, t * H, H).load(i, nt, tid);
+    ar = dx_in ? Row(dx_in, t * H, H).load(i, nt, tid) : zero;
+    float acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    for (int j0 = 0; j0 < k; j0 += kSlotBatch) {
+      u32x4_t v[kSlotBatch];
+      int row[kSlotBatch];
+#pragma unroll
+      for (int u = 0; u < kSlotBatch; ++u) {
+        row[u] = slot_row(pair_row + t * k, j0 + u, k, P);
+        v[u] = row[u] < 0 ? zero : Row(drows, static_cast<size_t>(row[u]) * H, H).load(i, nt, tid);
+      }
+#pragma unroll
+      for (int u = 0; u < kSlotBatch; ++u) {
+        float dot = 0.f;
+        if (row[u] >= 0) {
+          const float wj = w ? uniform_load(w + t * k + j0 + u) : 1.f;
+          float f[V], xv[V];
+          A::unpack(v[u], f);
+          if constexpr (DW) A::unpack(xr, xv);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            acc[e] = fmaf(wj, f[e], acc[e]);
+            if constexpr (DW) dot = fmaf(f[e], xv[e], dot);
+          }
+        }
+        if constexpr (DW)
+          if (j0 + u < k) add_dot(dots, j0 + u, dot, i == 0);
+      }
+    }
+    float a[V];
+    A::unpack(ar, a);
+#pragma unroll
+    for (int e = 0; e < V; ++e) a[e] += acc[e];
+    Row(dx, t * H, H).store(i, nt, tid, a);
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += 64) dlogits[t * E + e] = row[e];
+  if constexpr (DW) store_dots(dots, dw + t * k, k);
 }
 
-template <class A>
-static hipError_t dispatch_t(const moe_shape& s, const void* x, const int32_t* pair_row,
-                             const float* w, void* rows, hipStream_t st) {
-  typedef typename A::T E;
-  hipLaunchKernelGGL(k_dispatch<A>, dim3(s.T), dim3(256), 0, st, static_cast<const E*>(x), pair_row,
-                     w, static_cast<E*>(rows), s.H, s.top_k, s.T * s.top_k);
-  return hipGetLastError();
+// A workgroup per token: its gradient row times the weight to each slot's
+// row and, with DW, the slots' dot products with it.
+template <class A, bool DW>
+__global__ __launch_bounds__(1024) void k_combine_bwd(const void* dout, const void* y,
+                                                      const int32_t* pair_row, const float* w,
+                                                      void* dy, float* dw, int H, int k, int P) {
+  typedef RowRef<A, false> Row;
+  constexpr int V = A::VEC;
+  constexpr u32x4_t zero = {0u, 0u, 0u, 0u};
+  extern __shared__ float dots[];
+  const int nt = blockDim.x, tid = threadIdx.x;
+  const size_t t = blockIdx.x;
+  for (int i = 0; i * nt * V < H; ++i) {
+    const u32x4_t gr = Row(dout, t * H, H).load(i, nt, tid);
+    for (int j0 = 0; j0 < k; j0 += kSlotBatch) {
+      u32x4_t v[kSlotBatch];
+      int row[kSlotBatch];
+#pragma unroll
+      for (int u = 0; u < kSlotBatch; ++u) {
+        row[u] = slot_row(pair_row + t * k, j0 + u, k, P);
+        if constexpr (DW)
+          v[u] = row[u] < 0 ? zero : Row(y, static_cast<size_t>(row[u]) * H, H).load(i, nt, tid);
+      }
+#pragma unroll
+      for (int u = 0; u < kSlotBatch; ++u) {
+        float dot = 0.f;
+        if (row[u] >= 0) {
+          const float wj = uniform_load(w + t * k + j0 + u);
+          float g[V], f[V];
+          A::unpack(gr, g);
+          if constexpr (DW) {
+            A::unpack(v[u], f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) dot = fmaf(g[e], f[e], dot);
+          }
+#pragma unroll
+          for (int e = 0; e < V; ++e) g[e] *= wj;
+          Row(dy, static_cast<size_t>(row[u]) * H, H).store(i, nt, tid, g);
+        }
+        if constexpr (DW)
+          if (j0 + u < k) add_dot(dots, j0 + u, dot, i == 0);
+      }
+    }
+  }
+  if constexpr (DW) store_dots(dots, dw + t * k, k);
+}
+
+// A wave per token puts its row of dlogits together in LDS.
+__global__ __launch_bounds__(256) void k_route_bwd(const int32_t* ids, const float* w,
+                                                   const float* dw, float* dlogits, int T, int E,
+                                                   int k) {
+  __shared__ float rows[4][1024];
+  const int lane = threadIdx.x & 63;
+  const size_t t = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  float* row = rows[threadIdx.x >> 6];
+  const bool on = t < static_cast<size_t>(T);
+  for (int e = lane; e < E; e += 64) row[e] = 0.f;
+  float s = 0.f;
+  if (on)
+    for (int j = lane; j < k; j += 64) s = fmaf(w[t * k + j], dw[t * k + j], s);
+  s = wave_sum_f32(s);
+  __syncthreads();
+  if (on)
+    for (int j = lane; j < k; j += 64) {
+      const int e = ids[t * k + j];
+      if (e >= 0 && e < E) row[e] = w[t * k + j] * (dw[t * k + j] - s);
+    }
+  __syncthreads();
+  if (on)
+    for (int e = lane; e < E; e += 64) dlogits[t * E + e] = row[e];
 }
 
 hipError_t launch_dispatch(const moe_shape& s, const void* x, const int32_t* pair_row,
                            const float* w, void* rows, hipStream_t st) {
-  return s.act == MOE_DT_BF16 ? dispatch_t<RowBf16>(s, x, pair_row, w, rows, st)
-                              : dispatch_t<RowF32>(s, x, pair_row, w, rows, st);
+  const bool bf = s.act == MOE_DT_BF16;
+  const int parts = (s.H / (bf ? 8 : 4) + 63) / 64;
+  const unsigned blocks = (static_cast<unsigned>(s.T) * parts + 3) / 4;
+  auto kern = bf ? k_dispatch<RowBf16> : k_dispatch<RowF32>;
+  hipLaunchKernelGGL(kern, dim3(blocks), dim3(256), 0, st, x, pair_row, w, rows, s.T, s.H, s.top_k,
+                     s.T * s.top_k);
+  return hipGetLastError();
 }
 
-template <class A>
-static hipError_t dispatch_bwd_t(const moe_shape& s, const void* drows, const int32_t* pair_row,
-                                 const float* w, const void* x, const void* dx_in, void* dx,
-                                 float* dw, hipStream_t st) {
-  typedef typename A::T E;
-  hipLaunchKernelGGL(k_dispatch_bwd<A>, dim3(s.T), dim3(256), 0, st, static_cast<const E*>(drows),
-                     pair_row, w, static_cast<const E*>(x), static_cast<const E*>(dx_in),
-                     static_cast<E*>(dx), dw, s.H, s.top_k, s.T * s.top_k);
-  return hipGetLastError();
+// Threads of a token's workgroup: one chunk each, up to 1024.
+static int token_threads(const moe_shape& s) {
+  const int chunks = s.H / (s.act == MOE_DT_BF16 ? 8 : 4);
+  return std::min((chunks + 63) / 64 * 64, 1024);
+}
+
+// LDS of the dot products (at most 1024 slots x 16 waves x 4 bytes = 64 KB).
+static size_t dot_bytes(const moe_shape& s, int nt, const float* dw) {
+  return dw ? static_cast<size_t>(s.top_k) * (nt / 64) * sizeof(float) : 0;
 }
 
 hipError_t launch_dispatch_bwd(const moe_shape& s, const void* drows, const int32_t* pair_row,
                                const float* w, const void* x, const void* dx_in, void* dx,
                                float* dw, hipStream_t st) {
-  return s.act == MOE_DT_BF16
-             ? dispatch_bwd_t<RowBf16>(s, drows, pair_row, w, x, dx_in, dx, dw, st)
-             : dispatch_bwd_t<RowF32>(s, drows, pair_row, w, x, dx_in, dx, dw, st);
-}
-
-template <class A>
-static hipError_t combine_bwd_t(const moe_shape& s, const void* dout, const void* y,
-                                const int32_t* pair_row, const float* w, void* dy, float* dw,
-                                hipStream_t st) {
-  typedef typename A::T E;
-  hipLaunchKernelGGL(k_combine_bwd<A>, dim3(s.T), dim3(256), 0, st, static_cast<const E*>(dout),
-                     static_cast<const E*>(y), pair_row, w, static_cast<E*>(dy), dw, s.H, s.top_k,
-                     s.T * s.top_k);
+  const int nt = token_threads(s);
+  auto kern = s.act == MOE_DT_BF16
+                  ? (dw ? k_dispatch_bwd<RowBf16, true> : k_dispatch_bwd<RowBf16, false>)
+                  : (dw ? k_dispatch_bwd<RowF32, true> : k_dispatch_bwd<RowF32, false>);
+  hipLaunchKernelGGL(kern, dim3(s.T), dim3(nt), dot_bytes(s, nt, dw), st, drows, pair_row, w, x,
+                     dx_in, dx, dw, s.H, s.top_k, s.T * s.top_k);
   return hipGetLastError();
 }
 
 hipError_t launch_combine_bwd(const moe_shape& s, const void* dout, const void* y,
                               const int32_t* pair_row, const float* w, void* dy, float* dw,
                               hipStream_t st) {
-  return s.act == MOE_DT_BF16 ? combine_bwd_t<RowBf16>(s, dout, y, pair_row, w, dy, dw, st)
-                              : combine_bwd_t<RowF32>(s, dout, y, pair_row, w, dy, dw, st);
+  const int nt = token_threads(s);
+  auto kern = s.act == MOE_DT_BF16
+                  ? (dw ? k_combine_bwd<RowBf16, true> : k_combine_bwd<RowBf16, false>)
+                  : (dw ? k_combine_bwd<RowF32, true> : k_combine_bwd<RowF32, false>);
+  hipLaunchKernelGGL(kern, dim3(s.T), dim3(nt), dot_bytes(s, nt, dw), st, dout, y, pair_row, w, dy,
+                     dw, s.H, s.top_k, s.T * s.top_k);
+  return hipGetLastError();
 }
 
 hipError_t launch_route_bwd(const moe_shape& s, const int32_t* ids, const float* w,
                             const float* dw, float* dlogits, hipStream_t st) {
-  hipLaunchKernelGGL(k_route_bwd, dim3(s.T), dim3(64), 0, st, ids, w, dw, dlogits, s.E, s.top_k);
+  hipLaunchKernelGGL(k_route_bwd, dim3((s.T + 3) / 4), dim3(256), 0, st, ids, w, dw, dlogits, s.T,
+                     s.E, s.top_k);
   return hipGetLastError();
 }
 

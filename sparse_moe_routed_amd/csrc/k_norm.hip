@@ -21,7 +21,7 @@ struct FwdArgs {
 // (weights: offset 1), so that nothing but loads depends on it.
 template <class A, bool WAVE, int C, bool COMBINE, bool ODD, int GATE>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
-  typedef typename A::T E;
+  typedef RowRef<A, ODD> Row;
   constexpr int V = A::VEC;
   __shared__ float red[WAVE ? 1 : 2][16];
   const int nt = WAVE ? 64 : blockDim.x;
@@ -33,12 +33,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
   const size_t o = static_cast<size_t>(t) * H;
   const uint32_t flags = p.n.flags;
   const bool normed = !(flags & MOE_N_NO_NORM);
-  auto load = [&](const void* m, size_t at, int i) {
-    return load_chunk<A, ODD>(static_cast<const E*>(m) + at, i * nt + tid, H);
-  };
-  auto store = [&](void* m, int i, const float(&x)[V]) {
-    store_chunk<A, ODD>(static_cast<E*>(m) + o, i * nt + tid, H, x);
-  };
+  auto load = [&](const void* m, size_t at, int i) { return Row(m, at, H).load(i, nt, tid); };
+  auto store = [&](void* m, int i, const float(&x)[V]) { Row(m, o, H).store(i, nt, tid, x); };
 
   // everything is requested before the first use where registers allow
   constexpr bool EARLY = C <= (WAVE ? 8 : 2);
@@ -62,12 +58,11 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
       float w[KB];
 #pragma unroll
       for (int u = 0; u < KB; ++u) {
-        const int r = j0 + u < p.a.k ? pr[j0 + u] : -1;
-        const bool on = r >= 0 && r < p.P;
-        w[u] = on ? tw[j0 + u] : 0.f;
+        const int r = slot_row(pr, j0 + u, p.a.k, p.P);
+        w[u] = r >= 0 ? uniform_load(tw + j0 + u) : 0.f;
 #pragma unroll
         for (int i = 0; i < C; ++i)
-          y[u][i] = on ? load(p.a.y, static_cast<size_t>(r) * H, i) : zero;
+          y[u][i] = r >= 0 ? load(p.a.y, static_cast<size_t>(r) * H, i) : zero;
       }
 #pragma unroll
       for (int u = 0; u < KB; ++u)
@@ -97,7 +92,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
   }
   float gt = 1.f;
   if (flags & MOE_N_GATE_TOKEN) {
-    gt = static_cast<const float*>(p.a.gate)[t];
+    gt = uniform_load(static_cast<const float*>(p.a.gate) + t);
     if (flags & MOE_N_GATE_SIGMOID) gt = sigmoid(gt);
   }
   float rs = 1.f;

@@ -23,11 +23,11 @@ struct BwdArgs {
 // zeros (weights: offset 1), so that nothing but loads depends on it.
 template <class A, bool WAVE, int C, bool ODD, int GATE>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
-  typedef typename A::T E;
+  typedef RowRef<A, ODD> Row;
   constexpr int V = A::VEC;
   constexpr bool KEEP = WAVE || C <= 2;
   __shared__ float2 red[2][WAVE ? 1 : 16];
-  extern __shared__ float colsum[];   // WAVE: [H], the workgroup's dw
+  extern __shared__ float colsum[];   // WAVE: the workgroup's dw
   const int nt = WAVE ? 64 : blockDim.x;
   const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
   const int wave = WAVE ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
@@ -37,9 +37,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
   const bool normed = !(flags & MOE_N_NO_NORM), sig = flags & MOE_N_GATE_SIGMOID;
   constexpr bool full = GATE != kGateRow;
   const float bs = p.n.branch_scale;
-  auto load = [&](const void* m, size_t at, int i) {
-    return load_chunk<A, ODD>(static_cast<const E*>(m) + at, i * nt + tid, H);
-  };
+  auto load = [&](const void* m, size_t at, int i) { return Row(m, at, H).load(i, nt, tid); };
   float acc[C][V];
 #pragma unroll
   for (int i = 0; i < C; ++i)
@@ -67,7 +65,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
       }
     float gt = 1.f;
     if (flags & MOE_N_GATE_TOKEN) {
-      gt = static_cast<const float*>(p.a.gate)[t];
+      gt = uniform_load(static_cast<const float*>(p.a.gate) + t);
       if (sig) gt = sigmoid(gt);
     }
     auto gate = [&](int i, float(&g)[V]) {
@@ -127,7 +125,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
             r[e] = bs * d[e] * z[e] * w[e];
             if constexpr (GATE == kGateFullSigmoid) r[e] *= g[e] * (1.f - g[e]);
           }
-          store_chunk<A, ODD>(static_cast<E*>(p.a.dgate) + o, i * nt + tid, H, r);
+          Row(p.a.dgate, o, H).store(i, nt, tid, r);
         }
       }
       float sv[V];
@@ -139,25 +137,25 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
         r[e] = rs * fmaf(-z[e], c, d[e] * w[e]);
         r[e] = fmaf(p.n.residual_scale, sv[e], r[e]);
       }
-      store_chunk<A, ODD>(static_cast<E*>(p.a.dz) + o, i * nt + tid, H, r);
+      Row(p.a.dz, o, H).store(i, nt, tid, r);
     }
   }
   if (!p.a.dw) return;
-  float* part = p.a.part + static_cast<size_t>(blockIdx.x) * H;
+  // rows of `part` and colsum are norm_part_pitch(H) long: whole chunks
+  const int pitch = norm_part_pitch(H);
+  float* part = p.a.part + static_cast<size_t>(blockIdx.x) * pitch;
   // WAVE: the waves add their sums in turn, the last one writes
   for (int k = 0; k < waves; ++k) {
     if (k == wave)
 #pragma unroll
       for (int i = 0; i < C; ++i)
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int h = (i * nt + tid) * V + e;
-          if (h < H) {
-            const float v = k == 0 ? acc[i][e] : colsum[h] + acc[i][e];
-            if (k == waves - 1)
-              part[h] = v;
-            else
-              colsum[h] = v;
+        for (int q = 0; q < V; q += 4) {
+          const int h = (i * nt + tid) * V + q;
+          if (h < pitch) {
+            f32x4_t v = {acc[i][q], acc[i][q + 1], acc[i][q + 2], acc[i][q + 3]};
+            if (k > 0) v += *reinterpret_cast<f32x4_t*>(colsum + h);
+            *reinterpret_cast<f32x4_t*>((k == waves - 1 ? part : colsum) + h) = v;
           }
         }
     if (k < waves - 1) __syncthreads();
@@ -167,14 +165,15 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
 // dw[h] = sum over G rows of part: 64 columns per workgroup, its 16 waves
 // take the rows in turn and add up in LDS, in wave order.
 __global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part,
-                                                  float* __restrict__ dw, int G, int H) {
+                                                  float* __restrict__ dw, int G, int H,
+                                                  int pitch) {
   __shared__ float sum[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int h = blockIdx.x * 64 + lane;
   float s = 0.f;
   if (h < H) {
 #pragma unroll 8
-    for (int g = wave; g < G; g += 16) s += part[static_cast<size_t>(g) * H + h];
+    for (int g = wave; g < G; g += 16) s += part[static_cast<size_t>(g) * pitch + h];
   }
   sum[wave][lane] = s;
   __syncthreads();
@@ -215,7 +214,7 @@ static void bwd(const BwdArgs& p, int G, hipStream_t st) {
     nt = ((chunks + C - 1) / C + 63) / 64 * 64;
   }
   auto kern = H % A::VEC ? bwd_kernel<A, true, GATE>(wave, C) : bwd_kernel<A, false, GATE>(wave, C);
-  hipLaunchKernelGGL(kern, dim3(G), dim3(nt), wave && p.a.dw ? H * sizeof(float) : 0, st, p);
+  hipLaunchKernelGGL(kern, dim3(G), dim3(nt), wave && p.a.dw ? norm_part_pitch(H) * sizeof(float) : 0, st, p);
 }
 
 template <class A>
@@ -240,7 +239,8 @@ hipError_t launch_norm_bwd(const moe_norm& n, const NormBwd& a, hipStream_t st) 
     if (e != hipSuccess) return e;
   }
   if (a.dw)
-    hipLaunchKernelGGL(k_norm_dw, dim3((n.H + 63) / 64), dim3(1024), 0, st, a.part, a.dw, G, n.H);
+    hipLaunchKernelGGL(k_norm_dw, dim3((n.H + 63) / 64), dim3(1024), 0, st, a.part, a.dw, G, n.H,
+                       norm_part_pitch(n.H));
   return hipGetLastError();
 }
 

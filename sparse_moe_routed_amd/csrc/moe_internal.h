@@ -152,10 +152,11 @@ struct NormFwd {
 struct NormBwd {
   const void *dout, *z, *w, *gate, *dres;
   void *dz, *dgate;
-  float *dw, *part;   // part: float [norm_bwd_groups][H]
+  float *dw, *part;   // part: float [norm_bwd_groups][norm_part_pitch(H)]
 };
 constexpr int kNormWaves = 4;             // rows at a time of a gradient workgroup (wave per row)
 bool norm_bwd_wave(const moe_norm& n);   // a row is one wave's work
+constexpr int norm_part_pitch(int H) { return (H + 7) / 8 * 8; }
 int norm_bwd_groups(const moe_norm& n);   // workgroups of the gradient kernel
 hipError_t launch_norm_fwd(const moe_norm& n, const NormFwd& a, hipStream_t st);
 hipError_t launch_norm_bwd(const moe_norm& n, const NormBwd& a, hipStream_t st);

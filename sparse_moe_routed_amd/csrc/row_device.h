@@ -10,6 +10,14 @@ namespace moe {
 // global memory takes 16-byte accesses at element alignment.
 typedef u32x4_t u32x4_e2 __attribute__((aligned(2)));
 
+// A value of an input at a wave-uniform address, through the scalar cache: no
+// output of a kernel overlaps its inputs, so the value cannot change.
+template <typename T>
+__device__ __forceinline__ T uniform_load(const T* p) {
+  typedef const T __attribute__((address_space(4))) * const_ptr;
+  return *(const_ptr)(reinterpret_cast<uintptr_t>(p));
+}
+
 struct RowBf16 {
   typedef uint16_t T;
   static constexpr int VEC = 8;
@@ -54,38 +62,67 @@ struct RowF32 {
   }
 };
 
-// 16-byte chunk c of a row of H elements, zeros past its end.  ODD: H is no
-// multiple of VEC, so the last chunk is taken element by element.
+// One row of a matrix, read and written in 16-byte chunks: chunk i * nt + tid
+// by thread tid of nt.  Chunks past the row read as zeros and are not
+// written.  The row must be uniform over the wave.
+//
+// ODD == false (H a multiple of VEC): a raw buffer of the row's bytes, whose
+// bounds check takes the place of a branch per chunk, with a scalar base and
+// one offset register for all chunks (wide rows otherwise held a 64-bit
+// address and a predicate per chunk and matrix, and spilled).
 template <class A, bool ODD>
-__device__ __forceinline__ u32x4_t load_chunk(const typename A::T* row, int c, int H) {
-  constexpr int V = A::VEC;
-  if constexpr (!ODD) {
-    return c * V < H ? ld16(row + c * V) : u32x4_t{0u, 0u, 0u, 0u};
-  } else {
-    if ((c + 1) * V <= H) return *reinterpret_cast<const u32x4_e2*>(row + c * V);
+struct RowRef {
+  typedef typename A::T T;
+  static constexpr int V = A::VEC;
+  __amdgpu_buffer_rsrc_t rs;
+  __device__ __forceinline__ RowRef(const void* m, size_t at, int H)
+      : rs(__builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(static_cast<const T*>(m) + at), 0,
+                                             H * static_cast<int>(sizeof(T)), 0x00020000)) {}
+  __device__ __forceinline__ u32x4_t load(int i, int nt, int tid) const {
+    return __builtin_amdgcn_raw_buffer_load_b128(rs, tid * 16, i * nt * 16, 0);
+  }
+  __device__ __forceinline__ void store(int i, int nt, int tid, const float (&v)[V]) const {
+    store_raw(i, nt, tid, A::pack(v));
+  }
+  // The whole offset goes into the vector register.  With a scalar offset the
+  // compiler puts no wait state between a 16-byte buffer store and the next
+  // instruction, and where that one overwrote the data registers, some lanes
+  // stored the new first word (seen now and then in 65536-wide float32 rows:
+  // values of chunk i + 1 in chunk i).
+  __device__ __forceinline__ void store_raw(int i, int nt, int tid, u32x4_t v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v, rs, (i * nt + tid) * 16, 0, 0);
+  }
+};
+
+// ODD: rows start at any element; the chunk that the row's end cuts is taken
+// element by element.
+template <class A>
+struct RowRef<A, true> {
+  typedef typename A::T T;
+  static constexpr uint32_t V = A::VEC;
+  T* row;
+  uint32_t H;
+  __device__ __forceinline__ RowRef(const void* m, size_t at, int len)
+      : row(const_cast<T*>(static_cast<const T*>(m)) + at), H(len) {}
+  __device__ __forceinline__ u32x4_t load(int i, int nt, int tid) const {
+    const uint32_t h = static_cast<uint32_t>(i * nt + tid) * V;
+    if (h + V <= H) return *reinterpret_cast<const u32x4_e2*>(row + h);
     float v[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = c * V + i < H ? A::get(row[c * V + i]) : 0.f;
+    for (uint32_t e = 0; e < V; ++e) v[e] = h + e < H ? A::get(row[h + e]) : 0.f;
     return A::pack(v);
   }
-}
-
-template <class A, bool ODD>
-__device__ __forceinline__ void store_chunk(typename A::T* row, int c, int H,
-                                            const float (&v)[A::VEC]) {
-  constexpr int V = A::VEC;
-  if constexpr (!ODD) {
-    if (c * V < H) *reinterpret_cast<u32x4_t*>(row + c * V) = A::pack(v);
-  } else {
-    if ((c + 1) * V <= H) {
-      *reinterpret_cast<u32x4_e2*>(row + c * V) = A::pack(v);
+  __device__ __forceinline__ void store(int i, int nt, int tid, const float (&v)[V]) const {
+    const uint32_t h = static_cast<uint32_t>(i * nt + tid) * V;
+    if (h + V <= H) {
+      *reinterpret_cast<u32x4_e2*>(row + h) = A::pack(v);
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (c * V + i < H) row[c * V + i] = A::put(v[i]);
+      for (uint32_t e = 0; e < V; ++e)
+        if (h + e < H) row[h + e] = A::put(v[e]);
     }
   }
-}
+};
 
 // Sums of one or two values per thread over the threads of a row, in a fixed
 // association, the results in every thread.  WAVE: the row is one wave; else
@@ -120,6 +157,13 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2* slot) {
 
 __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + expf(-g));
+}
+
+// The row that pair p of a token's k slots has, or -1 when it is dropped
+// (outside [0, P)) or j is past the last slot.
+__device__ __forceinline__ int slot_row(const int32_t* pair_row, int j, int k, int P) {
+  const int r = j < k ? uniform_load(pair_row + j) : -1;
+  return r >= 0 && r < P ? r : -1;
 }
 
 // Full gates of the norm kernels (a token gate is a factor of the whole row)
