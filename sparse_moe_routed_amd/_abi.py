@@ -149,10 +149,27 @@ def ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """Function returning the handle of torch's current stream.  torch's
+    raw-stream query takes 0.3 us of host time, building a Stream object 2.8 us
+    (most of a small call)."""
+    global _raw_stream
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = torch.cuda.current_device
+    if raw is None:
+        _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
+    else:
+        _raw_stream = lambda: raw(device())
+    return _raw_stream
+
+
 def stream_handle(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return (_raw_stream or _current_stream())()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -352,23 +369,23 @@ def _torch_types():
 
 def _check_tensors(stream, args) -> int:
     """Status of (tensor, dtype, elements) triples; addresses and None pass."""
-    device, memory = None, 0
+    device, memory = -2, 0
     for t, dtype, n in args:
-        if t is None or isinstance(t, int):
+        if t is None or type(t) is int:
             continue
         if t.dtype is not dtype:
             return 3
         if t.numel() != n or not t.is_contiguous():
             return 2
-        if not t.is_cuda:
-            memory = 12
-            continue
-        if device is None:
-            device = _torch_types()[3]()
-            if stream is not None and not isinstance(stream, int) and stream.device_index != device:
+        at = t.get_device()                     # -1: host memory
+        if at != device:
+            if device == -2 and at >= 0:
+                device = _torch_types()[3]()
+            if at != device:
                 memory = 12
-        if t.get_device() != device:
-            memory = 12
+    if stream is not None and device >= 0 and type(stream) is not int \
+            and stream.device_index != device:
+        memory = 12
     return memory
 
 

@@ -170,29 +170,44 @@ __global__ __launch_bounds__(1024) void k_combine_bwd(const void* dout, const vo
   if constexpr (DW) store_dots(dots, dw + t * k, k);
 }
 
-// A wave per token puts its row of dlogits together in LDS.
-__global__ __launch_bounds__(256) void k_route_bwd(const int32_t* ids, const float* w,
-                                                   const float* dw, float* dlogits, int T, int E,
+// A wave per token puts its row of dlogits together in LDS (only its own, so
+// no barrier: a wave's LDS operations stay in order).
+__global__ __launch_bounds__(256) void k_route_bwd(const int32_t* __restrict__ ids,
+                                                   const float* __restrict__ w,
+                                                   const float* __restrict__ dw,
+                                                   float* __restrict__ dlogits, int T, int E,
                                                    int k) {
-  __shared__ float rows[4][1024];
-  const int lane = threadIdx.x & 63;
-  const size_t t = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  float* row = rows[threadIdx.x >> 6];
-  const bool on = t < static_cast<size_t>(T);
-  for (int e = lane; e < E; e += 64) row[e] = 0.f;
-  float s = 0.f;
-  if (on)
-    for (int j = lane; j < k; j += 64) s = fmaf(w[t * k + j], dw[t * k + j], s);
+  extern __shared__ f32x4_t route_rows[];   // [4][pitch / 4]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, pitch = (E + 3) / 4 * 4;
+  const size_t t = static_cast<size_t>(blockIdx.x) * 4 + wave;
+  if (t >= static_cast<size_t>(T)) return;
+  // the first 64 slots in registers, requested together
+  int id = -1;
+  float wj = 0.f, dj = 0.f;
+  if (lane < k) {
+    id = ids[t * k + lane];
+    wj = w[t * k + lane];
+    dj = dw[t * k + lane];
+  }
+  f32x4_t* row4 = route_rows + wave * (pitch / 4);
+  float* row = reinterpret_cast<float*>(row4);
+  for (int e = lane; e < pitch / 4; e += 64) row4[e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  float s = wj * dj;
+  for (int j = lane + 64; j < k; j += 64) s = fmaf(w[t * k + j], dw[t * k + j], s);
   s = wave_sum_f32(s);
-  __syncthreads();
-  if (on)
-    for (int j = lane; j < k; j += 64) {
-      const int e = ids[t * k + j];
-      if (e >= 0 && e < E) row[e] = w[t * k + j] * (dw[t * k + j] - s);
-    }
-  __syncthreads();
-  if (on)
-    for (int e = lane; e < E; e += 64) dlogits[t * E + e] = row[e];
+  __builtin_amdgcn_wave_barrier();
+  if (id >= 0 && id < E) row[id] = wj * (dj - s);
+  for (int j = lane + 64; j < k; j += 64) {
+    const int e = ids[t * k + j];
+    if (e >= 0 && e < E) row[e] = w[t * k + j] * (dw[t * k + j] - s);
+  }
+  __builtin_amdgcn_wave_barrier();
+  float* out = dlogits + t * E;
+  if (E % 4 == 0) {
+    for (int e = lane; e < E / 4; e += 64) *reinterpret_cast<f32x4_t*>(out + 4 * e) = row4[e];
+  } else {
+    for (int e = lane; e < E; e += 64) out[e] = row[e];
+  }
 }
 
 hipError_t launch_dispatch(const moe_shape& s, const void* x, const int32_t* pair_row,
@@ -243,8 +258,9 @@ hipError_t launch_combine_bwd(const moe_shape& s, const void* dout, const void* 
 
 hipError_t launch_route_bwd(const moe_shape& s, const int32_t* ids, const float* w,
                             const float* dw, float* dlogits, hipStream_t st) {
-  hipLaunchKernelGGL(k_route_bwd, dim3((s.T + 3) / 4), dim3(256), 0, st, ids, w, dw, dlogits, s.T,
-                     s.E, s.top_k);
+  hipLaunchKernelGGL(k_route_bwd, dim3((s.T + 3) / 4), dim3(256),
+                     4 * ((s.E + 3) / 4 * 4) * sizeof(float), st, ids, w, dw, dlogits, s.T, s.E,
+                     s.top_k);
   return hipGetLastError();
 }
 

@@ -37,12 +37,21 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
   auto store = [&](void* m, int i, const float(&x)[V]) { Row(m, o, H).store(i, nt, tid, x); };
 
   // everything is requested before the first use where registers allow
-  constexpr bool EARLY = C <= (WAVE ? 8 : 2);
+  constexpr bool EARLY = WAVE || C <= 2;
   constexpr u32x4_t zero = {0u, 0u, 0u, 0u};
   auto weight = [&](int i) { return normed ? load(p.a.w, 0, i) : zero; };
   auto gate = [&](int i) { return load(p.a.gate, o, i); };
   auto residual = [&](int i) { return p.a.residual ? load(p.a.residual, o, i) : zero; };
   u32x4_t wr[EARLY ? C : 1], gr[EARLY ? C : 1], rr[EARLY ? C : 1], nr[EARLY ? C : 1];
+  if constexpr (EARLY) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      wr[i] = weight(i);
+      if constexpr (GATE != kGateRow) gr[i] = gate(i);
+      rr[i] = residual(i);
+      if (p.a.n_next) nr[i] = load(p.a.w_next, 0, i);
+    }
+  }
   float v[C][V];
   if constexpr (COMBINE) {
     // slots in batches: the batch's rows are all requested, then added, j ascending
@@ -80,15 +89,6 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
   } else {
 #pragma unroll
     for (int i = 0; i < C; ++i) A::unpack(load(p.a.z, o, i), v[i]);
-  }
-  if constexpr (EARLY) {
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      wr[i] = weight(i);
-      if constexpr (GATE != kGateRow) gr[i] = gate(i);
-      rr[i] = residual(i);
-      if (p.a.n_next) nr[i] = load(p.a.w_next, 0, i);
-    }
   }
   float gt = 1.f;
   if (flags & MOE_N_GATE_TOKEN) {
@@ -137,15 +137,13 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
 
 typedef void (*FwdKernel)(FwdArgs);
 
-template <class A, bool ODD, int GATE>
+template <bool ODD, int GATE>
 static FwdKernel fwd_wave(int C) {
   switch (C) {
-    case 1: return k_norm_fwd<A, true, 1, false, ODD, GATE>;
-    case 2: return k_norm_fwd<A, true, 2, false, ODD, GATE>;
-    case 3: return k_norm_fwd<A, true, 3, false, ODD, GATE>;
-    case 4:
-    case 5: return k_norm_fwd<A, true, 5, false, ODD, GATE>;
-    default: return k_norm_fwd<A, true, 8, false, ODD, GATE>;
+    case 1: return k_norm_fwd<RowBf16, true, 1, false, ODD, GATE>;
+    case 2: return k_norm_fwd<RowBf16, true, 2, false, ODD, GATE>;
+    case 3: return k_norm_fwd<RowBf16, true, 3, false, ODD, GATE>;
+    default: return k_norm_fwd<RowBf16, true, 5, false, ODD, GATE>;
   }
 }
 
@@ -164,17 +162,26 @@ template <class A, bool COMBINE, int GATE>
 static hipError_t fwd(const FwdArgs& p, hipStream_t st) {
   const int T = p.n.T, H = p.n.H, chunks = (H + A::VEC - 1) / A::VEC;
   const bool odd = H % A::VEC != 0;   // never with COMBINE: H % 128 == 0 there
-  if (!COMBINE && chunks <= 8 * 64) {
-    const int C = (chunks + 63) / 64, rows = T >= 1024 ? 4 : 1;
-    auto kern = odd ? fwd_wave<A, true, GATE>(C) : fwd_wave<A, false, GATE>(C);
-    hipLaunchKernelGGL(kern, dim3((T + rows - 1) / rows), dim3(64 * rows), 0, st, p);
-  } else {
-    int C = 1;
-    while (chunks > 1024 * C) C *= 2;
-    const int nt = ((chunks + C - 1) / C + 63) / 64 * 64;
-    auto kern = odd ? fwd_block<A, COMBINE, !COMBINE, GATE>(C) : fwd_block<A, COMBINE, false, GATE>(C);
-    hipLaunchKernelGGL(kern, dim3(T), dim3(nt), 0, st, p);
+  // A wave per row saves the barriers and is the faster one while there are
+  // rows to fill the card with single waves and a row is at most 5 chunks per
+  // lane; few rows finish sooner with a thread per chunk.  norm_out with a
+  // full gate, 2560 bf16: 1 row 4.4 us (wave) against 3.3 (workgroup), 512
+  // rows 6.0 / 5.8, 2048 rows 12.7 / 13.8, 32768 rows 117 / 126.  float32
+  // rows have twice the chunks: the workgroup is never slower there (4096 x
+  // 1024: 19.1 / 16.2 us).
+  if constexpr (!COMBINE && A::VEC == 8) {
+    if (T >= 1024 && chunks <= 5 * 64) {
+      const int C = (chunks + 63) / 64;
+      auto kern = odd ? fwd_wave<true, GATE>(C) : fwd_wave<false, GATE>(C);
+      hipLaunchKernelGGL(kern, dim3((T + 3) / 4), dim3(256), 0, st, p);
+      return hipGetLastError();
+    }
   }
+  int C = 1;
+  while (chunks > 1024 * C) C *= 2;
+  const int nt = ((chunks + C - 1) / C + 63) / 64 * 64;
+  auto kern = odd ? fwd_block<A, COMBINE, !COMBINE, GATE>(C) : fwd_block<A, COMBINE, false, GATE>(C);
+  hipLaunchKernelGGL(kern, dim3(T), dim3(nt), 0, st, p);
   return hipGetLastError();
 }
 

@@ -162,25 +162,27 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
   }
 }
 
-// dw[h] = sum over G rows of part: 64 columns per workgroup, its 16 waves
-// take the rows in turn and add up in LDS, in wave order.
+// dw[h] = sum over G rows of part: 32 columns per workgroup, each by 32
+// threads that take the rows in turn (up to 16 requested together), then
+// added in LDS in a fixed order.
 __global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part,
                                                   float* __restrict__ dw, int G, int H,
                                                   int pitch) {
-  __shared__ float sum[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int h = blockIdx.x * 64 + lane;
+  __shared__ float sum[32][33];
+  const int col = threadIdx.x & 31, by = threadIdx.x >> 5;
+  const int h = blockIdx.x * 32 + col;
   float s = 0.f;
   if (h < H) {
-#pragma unroll 8
-    for (int g = wave; g < G; g += 16) s += part[static_cast<size_t>(g) * pitch + h];
+#pragma unroll 16
+    for (int g = by; g < G; g += 32) s += part[static_cast<size_t>(g) * pitch + h];
   }
-  sum[wave][lane] = s;
+  sum[by][col] = s;
   __syncthreads();
-  if (wave == 0 && h < H) {
-    for (int i = 1; i < 16; ++i) s += sum[i][lane];
-    dw[h] = s;
-  }
+  // thread (col, by) now holds row col of column by
+  s = sum[col][by];
+#pragma unroll
+  for (int m = 16; m > 0; m /= 2) s += __shfl_xor(s, m, 32);
+  if (col == 0 && blockIdx.x * 32 + by < static_cast<unsigned>(H)) dw[blockIdx.x * 32 + by] = s;
 }
 
 typedef void (*BwdKernel)(BwdArgs);
@@ -239,7 +241,7 @@ hipError_t launch_norm_bwd(const moe_norm& n, const NormBwd& a, hipStream_t st) 
     if (e != hipSuccess) return e;
   }
   if (a.dw)
-    hipLaunchKernelGGL(k_norm_dw, dim3((n.H + 63) / 64), dim3(1024), 0, st, a.part, a.dw, G, n.H,
+    hipLaunchKernelGGL(k_norm_dw, dim3((n.H + 31) / 32), dim3(1024), 0, st, a.part, a.dw, G, n.H,
                        norm_part_pitch(n.H));
   return hipGetLastError();
 }

@@ -49,11 +49,14 @@ bool tiles128_ok(const moe_shape& s) {
          s.I % 128 == 0;
 }
 
-// In the gradient a wave holds rows of up to 320 16-byte chunks and their
-// column sums in registers; longer rows take a workgroup.
+// A wave per row (up to 5 16-byte chunks per lane, with their column sums in
+// registers) once there are enough rows; few rows finish sooner with a
+// workgroup each, and longer rows need one.  2560 bf16, with dw: 1 row 8.5 us
+// (wave) against 4.8 (workgroup), 512 rows 11.1 / 9.5, 4096 rows 21.7 / 22.7,
+// 32768 rows 98 / 122; 256 bf16: 2048 rows 6.6 / 7.7.
 bool norm_bwd_wave(const moe_norm& n) {
   const int vec = n.act == MOE_DT_BF16 ? 8 : 4;
-  return n.H <= 320 * vec;
+  return n.T >= 2048 && n.H <= 320 * vec;
 }
 
 // Workgroups of the norm gradient: each leaves one row of column sums.
