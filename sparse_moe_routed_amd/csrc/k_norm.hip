@@ -93,7 +93,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
   float gt = 1.f;
   if (flags & MOE_N_GATE_TOKEN) {
     gt = uniform_load(static_cast<const float*>(p.a.gate) + t);
-    if (flags & MOE_N_GATE_SIGMOID) gt = sigmoid(gt);
+    if (flags & MOE_N_GATE_SIGMOID) gt = sigmoid<true>(gt);
   }
   float rs = 1.f;
   if (normed) {
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
     for (int e = 0; e < V; ++e) {
       v[i][e] = v[i][e] * rs * (w[e] + offset) * factor;
       if constexpr (GATE == kGateFull) v[i][e] *= g[e];
-      if constexpr (GATE == kGateFullSigmoid) v[i][e] *= sigmoid(g[e]);
+      if constexpr (GATE == kGateFullSigmoid) v[i][e] *= sigmoid<A::VEC == 4>(g[e]);
       v[i][e] = fmaf(p.n.residual_scale, r[e], v[i][e]);
       ss = fmaf(v[i][e], v[i][e], ss);   // zeros past the row's end
     }

@@ -66,13 +66,16 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
     float gt = 1.f;
     if (flags & MOE_N_GATE_TOKEN) {
       gt = uniform_load(static_cast<const float*>(p.a.gate) + t);
-      if (sig) gt = sigmoid(gt);
+      if (sig) gt = sigmoid<true>(gt);
     }
+    // the full gate's factors; a sigmoid is kept for the second use
+    constexpr bool KEEP_G = KEEP && GATE == kGateFullSigmoid;
+    float gk[KEEP_G ? C : 1][V];
     auto gate = [&](int i, float(&g)[V]) {
       if constexpr (full) A::unpack(KEEP ? gr[i] : load(p.a.gate, o, i), g);
       if constexpr (GATE == kGateFullSigmoid)
 #pragma unroll
-        for (int e = 0; e < V; ++e) g[e] = sigmoid(g[e]);
+        for (int e = 0; e < V; ++e) g[e] = sigmoid<V == 4>(g[e]);
     };
     float ss = 0.f, s1 = 0.f;
 #pragma unroll
@@ -83,6 +86,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
       A::unpack(KEEP ? dr[i] : load(p.a.dout, o, i), d);
       A::unpack(KEEP ? wr[i] : load_w(i), w);
       gate(i, g);
+      if constexpr (KEEP_G)
+#pragma unroll
+        for (int e = 0; e < V; ++e) gk[i][e] = g[e];
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float dw = d[e] * (w[e] + offset);
@@ -96,7 +102,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         asm volatile("" : "+v"(zr[i]), "+v"(dr[i]), "+v"(wr[i]));
-        if constexpr (full) asm volatile("" : "+v"(gr[i]));
+        if constexpr (full && !KEEP_G) asm volatile("" : "+v"(gr[i]));
       }
     const float2 s = row_sum2<WAVE>(ss, s1, red[parity]);
     const float rs = normed ? rsqrtf(s.x / H + p.n.eps) : 1.f;
@@ -112,7 +118,12 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
       A::unpack(KEEP ? zr[i] : load(p.a.z, o, i), z);
       A::unpack(KEEP ? dr[i] : load(p.a.dout, o, i), d);
       A::unpack(KEEP ? wr[i] : load_w(i), w);
-      gate(i, g);
+      if constexpr (KEEP_G) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) g[e] = gk[i][e];
+      } else {
+        gate(i, g);
+      }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         z[e] *= rs;

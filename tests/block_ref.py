@@ -40,12 +40,14 @@ def _norm(z, ez, w, eps):
 
 def _gate(flags, gate, T):
     if not flags & (GATE_TOKEN | GATE_FULL):
-        return None, None, 0.0
+        return None, None, 0.0          # factor, slope, relative error
     raw = gate.double().reshape(T, -1)
     if flags & SIGMOID:
         G = 1 / (1 + torch.exp(-raw))
-        # expf and one division; the exponential's argument is exact
-        return G, torch.exp(-raw) * G * G, 8 * E
+        # exp2 of the rounded product g log2(e): half an ulp of an argument up to
+        # 1.45 |g| changes the exponential by at most |g| e relative to its value,
+        # then exp2, the addition and the reciprocal: 8 e
+        return G, torch.exp(-raw) * G * G, (8 + raw.abs()) * E
     return raw, torch.ones_like(raw), 0.0
 
 
@@ -94,13 +96,13 @@ def norm_bwd(dout, z, w, gate, dres, *, dtype, eps, offset, rscale, bscale, flag
     dz, edz = g, g.abs() * (5 * E + eg)
     if normed:
         c = (g * zh).mean(1, keepdim=True)
-        ec = (g * zh).abs().mean(1, keepdim=True) * ((L + 10) * E + eg + rel)
+        ec = ((g * zh).abs() * ((L + 10) * E + eg + rel)).mean(1, keepdim=True)
         dz = rs * (g - zh * c)
         mag = rs * (g.abs() + (zh * c).abs())
         edz = mag * (8 * E + eg + 2 * rel) + rs * zh.abs() * ec
         t = db * G1 * zh
         # rows of a workgroup one after the other, then the workgroups
-        res["dw"] = (t.sum(0), t.abs().sum(0) * ((T + 8) * E + eg + rel) + TINY * T)
+        res["dw"] = (t.sum(0), (t.abs() * ((T + 8) * E + eg + rel)).sum(0) + TINY * T)
     if dres is not None:
         d = rscale * dres.double()
         dz, edz = dz + d, edz + (dz + d).abs() * E + d.abs() * E
@@ -112,7 +114,7 @@ def norm_bwd(dout, z, w, gate, dres, *, dtype, eps, offset, rscale, bscale, flag
         edge = (db * zh * W).abs() * G1.abs() * (2 * E) if flags & SIGMOID else 0.0
         if flags & GATE_TOKEN:
             val = t.sum(1)
-            err = t.abs().sum(1) * ((L + 4) * E + rd) + (edge.sum(1) if flags & SIGMOID else 0.0)
+            err = (t.abs() * ((L + 4) * E + rd)).sum(1) + (edge.sum(1) if flags & SIGMOID else 0.0)
             res["dgate"] = (val, err + TINY * H)
         else:
             res["dgate"] = (t, t.abs() * (rd + u_of(dtype)) + edge + TINY)

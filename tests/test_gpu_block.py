@@ -133,6 +133,15 @@ def test_norm_out(T, H, flags, act):
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("flags", FLAGS)
+@pytest.mark.parametrize("T,H", [(1024, 520), (2048, 8), (2050, 1001), (2051, 1536), (2304, 2560),
+                                 (2049, 2561), (4097, 33), (2050, 1280), (2050, 257)])
+def test_norm_out_many_rows(T, H, flags, act):
+    """From 1024 (2048) rows on a row is one wave's work."""
+    run_norm_out(T, H, act, flags, nxt=H % 2 == 0, residual=H != 520)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("H", [1, 5, 8, 63, 512, 513, 1537, 2049, 4100, 8192, 8201, 20480, 65535, 65536])
 def test_norm_out_widths(H, act):
     run_norm_out(4, H, act, FULL | SIG)
