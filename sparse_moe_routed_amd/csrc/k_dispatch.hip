@@ -11,7 +11,7 @@ namespace moe {
 
 // One wave per 64 chunks of a token's row: the chunk stays in registers while
 // it is stored to each of the k rows.
-template <class A>
+template <class A, bool WEIGHTED>
 __global__ __launch_bounds__(256) void k_dispatch(const void* x, const int32_t* pair_row,
                                                   const float* w, void* rows, int T, int H, int k,
                                                   int P) {
@@ -23,18 +23,18 @@ __global__ __launch_bounds__(256) void k_dispatch(const void* x, const int32_t* 
   const int lane = threadIdx.x & 63;
   const u32x4_t v = RowRef<A, false>(x, static_cast<size_t>(t) * H, H).load(c, 64, lane);
   const int32_t* pr = pair_row + static_cast<size_t>(t) * k;
-  for (int j0 = 0; j0 < k; j0 += 8) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int r = slot_row(pr, j0 + u, k, P);
+  for (int j0 = 0; j0 < k; j0 += 64) {
+    const Slots<WEIGHTED> slots(pr, w + static_cast<size_t>(t) * k, j0, k, P);
+    const int n = min(k - j0, 64);
+    for (int u = 0; u < n; ++u) {
+      const int r = slots.row(u);
       if (r < 0) continue;
       const RowRef<A, false> row(rows, static_cast<size_t>(r) * H, H);
-      if (w) {
-        const float wj = uniform_load(w + static_cast<size_t>(t) * k + j0 + u);
+      if constexpr (WEIGHTED) {
         float f[V];
         A::unpack(v, f);
 #pragma unroll
-        for (int e = 0; e < V; ++e) f[e] *= wj;
+        for (int e = 0; e < V; ++e) f[e] *= slots.weight(u);
         row.store(c, 64, lane, f);
       } else {
         row.store_raw(c, 64, lane, v);
@@ -70,7 +70,7 @@ __device__ __forceinline__ void store_dots(const float* dots, float* dw, int k) 
 
 // A workgroup per token: the sum over its slots' rows and, with DW, each
 // row's dot product with x.
-template <class A, bool DW>
+template <class A, bool WEIGHTED, bool DW>
 __global__ __launch_bounds__(1024) void k_dispatch_bwd(const void* drows, const int32_t* pair_row,
                                                        const float* w, const void* x,
                                                        const void* dx_in, void* dx, float* dw,
@@ -90,17 +90,17 @@ __global__ __launch_bounds__(1024) void k_dispatch_bwd(const void* drows, const 
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
     for (int j0 = 0; j0 < k; j0 += kSlotBatch) {
       u32x4_t v[kSlotBatch];
-      int row[kSlotBatch];
+      const Slots<WEIGHTED> slots(pair_row + t * k, w + t * k, j0, k, P);
 #pragma unroll
-      for (int u = 0; u < kSlotBatch; ++u) {
-        row[u] = slot_row(pair_row + t * k, j0 + u, k, P);
-        v[u] = row[u] < 0 ? zero : Row(drows, static_cast<size_t>(row[u]) * H, H).load(i, nt, tid);
-      }
+      for (int q = 0; q < kSlotBatch; q += 4)
+        if (j0 + q < k)
+#pragma unroll
+          for (int u = q; u < q + 4; ++u) v[u] = Row::slot(drows, slots.row(u), H).load(i, nt, tid);
 #pragma unroll
       for (int u = 0; u < kSlotBatch; ++u) {
         float dot = 0.f;
-        if (row[u] >= 0) {
-          const float wj = w ? uniform_load(w + t * k + j0 + u) : 1.f;
+        if (slots.row(u) >= 0) {
+          const float wj = slots.weight(u);
           float f[V], xv[V];
           A::unpack(v[u], f);
           if constexpr (DW) A::unpack(xr, xv);
@@ -131,7 +131,6 @@ __global__ __launch_bounds__(1024) void k_combine_bwd(const void* dout, const vo
                                                       void* dy, float* dw, int H, int k, int P) {
   typedef RowRef<A, false> Row;
   constexpr int V = A::VEC;
-  constexpr u32x4_t zero = {0u, 0u, 0u, 0u};
   extern __shared__ float dots[];
   const int nt = blockDim.x, tid = threadIdx.x;
   const size_t t = blockIdx.x;
@@ -139,18 +138,19 @@ __global__ __launch_bounds__(1024) void k_combine_bwd(const void* dout, const vo
     const u32x4_t gr = Row(dout, t * H, H).load(i, nt, tid);
     for (int j0 = 0; j0 < k; j0 += kSlotBatch) {
       u32x4_t v[kSlotBatch];
-      int row[kSlotBatch];
+      const Slots<true> slots(pair_row + t * k, w + t * k, j0, k, P);
+      if constexpr (DW)
 #pragma unroll
-      for (int u = 0; u < kSlotBatch; ++u) {
-        row[u] = slot_row(pair_row + t * k, j0 + u, k, P);
-        if constexpr (DW)
-          v[u] = row[u] < 0 ? zero : Row(y, static_cast<size_t>(row[u]) * H, H).load(i, nt, tid);
-      }
+        for (int q = 0; q < kSlotBatch; q += 4)
+          if (j0 + q < k)
+#pragma unroll
+            for (int u = q; u < q + 4; ++u) v[u] = Row::slot(y, slots.row(u), H).load(i, nt, tid);
 #pragma unroll
       for (int u = 0; u < kSlotBatch; ++u) {
         float dot = 0.f;
-        if (row[u] >= 0) {
-          const float wj = uniform_load(w + t * k + j0 + u);
+        const int r = slots.row(u);
+        if (r >= 0) {
+          const float wj = slots.weight(u);
           float g[V], f[V];
           A::unpack(gr, g);
           if constexpr (DW) {
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(1024) void k_combine_bwd(const void* dout, const vo
           }
 #pragma unroll
           for (int e = 0; e < V; ++e) g[e] *= wj;
-          Row(dy, static_cast<size_t>(row[u]) * H, H).store(i, nt, tid, g);
+          Row(dy, static_cast<size_t>(r) * H, H).store(i, nt, tid, g);
         }
         if constexpr (DW)
           if (j0 + u < k) add_dot(dots, j0 + u, dot, i == 0);
@@ -215,7 +215,8 @@ hipError_t launch_dispatch(const moe_shape& s, const void* x, const int32_t* pai
   const bool bf = s.act == MOE_DT_BF16;
   const int parts = (s.H / (bf ? 8 : 4) + 63) / 64;
   const unsigned blocks = (static_cast<unsigned>(s.T) * parts + 3) / 4;
-  auto kern = bf ? k_dispatch<RowBf16> : k_dispatch<RowF32>;
+  auto kern = bf ? (w ? k_dispatch<RowBf16, true> : k_dispatch<RowBf16, false>)
+                 : (w ? k_dispatch<RowF32, true> : k_dispatch<RowF32, false>);
   hipLaunchKernelGGL(kern, dim3(blocks), dim3(256), 0, st, x, pair_row, w, rows, s.T, s.H, s.top_k,
                      s.T * s.top_k);
   return hipGetLastError();
@@ -236,9 +237,11 @@ hipError_t launch_dispatch_bwd(const moe_shape& s, const void* drows, const int3
                                const float* w, const void* x, const void* dx_in, void* dx,
                                float* dw, hipStream_t st) {
   const int nt = token_threads(s);
-  auto kern = s.act == MOE_DT_BF16
-                  ? (dw ? k_dispatch_bwd<RowBf16, true> : k_dispatch_bwd<RowBf16, false>)
-                  : (dw ? k_dispatch_bwd<RowF32, true> : k_dispatch_bwd<RowF32, false>);
+  const bool bf = s.act == MOE_DT_BF16;
+  auto kern = dw   ? (bf ? k_dispatch_bwd<RowBf16, true, true> : k_dispatch_bwd<RowF32, true, true>)
+              : w  ? (bf ? k_dispatch_bwd<RowBf16, true, false> : k_dispatch_bwd<RowF32, true, false>)
+              : bf ? k_dispatch_bwd<RowBf16, false, false>
+                   : k_dispatch_bwd<RowF32, false, false>;
   hipLaunchKernelGGL(kern, dim3(s.T), dim3(nt), dot_bytes(s, nt, dw), st, drows, pair_row, w, x,
                      dx_in, dx, dw, s.H, s.top_k, s.T * s.top_k);
   return hipGetLastError();

@@ -28,7 +28,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
   const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
   const int t = WAVE ? __builtin_amdgcn_readfirstlane(blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6))
                      : blockIdx.x;
-  if (t >= p.n.T) return;
+  if (WAVE && t >= p.n.T) return;
   const int H = p.n.H;
   const size_t o = static_cast<size_t>(t) * H;
   const uint32_t flags = p.n.flags;
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
   float v[C][V];
   if constexpr (COMBINE) {
     // slots in batches: the batch's rows are all requested, then added, j ascending
-    constexpr int KB = C == 1 ? 16 : C == 2 ? 8 : C == 4 ? 2 : 1;
+    constexpr int KB = C == 1 ? 16 : C == 2 ? 4 : C == 4 ? 2 : 1;
 #pragma unroll
     for (int i = 0; i < C; ++i)
 #pragma unroll
@@ -64,24 +64,29 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
     const float* tw = p.a.topk_w + static_cast<size_t>(t) * p.a.k;
     for (int j0 = 0; j0 < p.a.k; j0 += KB) {
       u32x4_t y[KB][C];
-      float w[KB];
+      const Slots<true> slots(pr, tw, j0, p.a.k, p.P);
+      constexpr int G = KB < 4 ? KB : 4;   // slots past the last one go in groups
 #pragma unroll
-      for (int u = 0; u < KB; ++u) {
-        const int r = slot_row(pr, j0 + u, p.a.k, p.P);
-        w[u] = r >= 0 ? uniform_load(tw + j0 + u) : 0.f;
+      for (int q = 0; q < KB; q += G)
+        if (j0 + q < p.a.k)
 #pragma unroll
-        for (int i = 0; i < C; ++i)
-          y[u][i] = r >= 0 ? load(p.a.y, static_cast<size_t>(r) * H, i) : zero;
-      }
+          for (int u = q; u < q + G; ++u)
 #pragma unroll
-      for (int u = 0; u < KB; ++u)
+            for (int i = 0; i < C; ++i) y[u][i] = Row::slot(p.a.y, slots.row(u), H).load(i, nt, tid);
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-          float f[V];
-          A::unpack(y[u][i], f);
+      for (int q = 0; q < KB; q += G)
+        if (j0 + q < p.a.k)
 #pragma unroll
-          for (int e = 0; e < V; ++e) v[i][e] = fmaf(w[u], f[e], v[i][e]);
-        }
+          for (int u = q; u < q + G; ++u) {
+            const float w = slots.weight(u);
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+              float f[V];
+              A::unpack(y[u][i], f);
+#pragma unroll
+              for (int e = 0; e < V; ++e) v[i][e] = fmaf(w, f[e], v[i][e]);
+            }
+          }
     }
     if (p.a.z_out)
 #pragma unroll

@@ -78,6 +78,11 @@ struct RowRef {
   __device__ __forceinline__ RowRef(const void* m, size_t at, int H)
       : rs(__builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(static_cast<const T*>(m) + at), 0,
                                              H * static_cast<int>(sizeof(T)), 0x00020000)) {}
+  // row r of m, or nothing at all (loads give zeros) for r < 0
+  static __device__ __forceinline__ RowRef slot(const void* m, int r, int H) {
+    RowRef ref(m, static_cast<size_t>(max(r, 0)) * H, r < 0 ? 0 : H);
+    return ref;
+  }
   __device__ __forceinline__ u32x4_t load(int i, int nt, int tid) const {
     return __builtin_amdgcn_raw_buffer_load_b128(rs, tid * 16, i * nt * 16, 0);
   }
@@ -164,12 +169,29 @@ __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// The row that pair p of a token's k slots has, or -1 when it is dropped
-// (outside [0, P)) or j is past the last slot.
-__device__ __forceinline__ int slot_row(const int32_t* pair_row, int j, int k, int P) {
-  const int r = j < k ? uniform_load(pair_row + j) : -1;
-  return r >= 0 && r < P ? r : -1;
-}
+// Rows and weights of a token's slots j0 .. j0 + 63, one per lane: row -1
+// and weight 0 for a dropped pair (row outside [0, P)) and past slot k - 1.
+// One vector load each; row(u) and weight(u) are scalars read from a lane
+// where they are needed (a scalar load per slot took a round trip each, all
+// of them up front took more scalar registers than there are).
+template <bool WEIGHTED>
+struct Slots {
+  int r;
+  float w;
+  __device__ __forceinline__ Slots(const int32_t* pair_row, const float* weights, int j0, int k,
+                                   int P) {
+    const int j = j0 + (threadIdx.x & 63);
+    r = j < k ? pair_row[j] : -1;
+    w = 1.f;
+    if constexpr (WEIGHTED) w = j < k ? weights[j] : 0.f;
+    if (r < 0 || r >= P) r = -1;
+    if (r < 0) w = 0.f;
+  }
+  __device__ __forceinline__ int row(int u) const { return __builtin_amdgcn_readlane(r, u); }
+  __device__ __forceinline__ float weight(int u) const {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), u));
+  }
+};
 
 // Full gates of the norm kernels (a token gate is a factor of the whole row)
 constexpr int kGateRow = 0, kGateFull = 1, kGateFullSigmoid = 2;
