@@ -21,7 +21,8 @@ __global__ __launch_bounds__(256) void k_dispatch(const void* x, const int32_t* 
   const int t = unit / parts, c = unit - t * parts;
   if (t >= T) return;
   const int lane = threadIdx.x & 63;
-  const u32x4_t v = RowRef<A, false>(x, static_cast<size_t>(t) * H, H).load(c, 64, lane);
+  typedef RowRef<A, false, false> Row;
+  const u32x4_t v = Row(x, static_cast<size_t>(t) * H, H).load(c, 64, lane);
   const int32_t* pr = pair_row + static_cast<size_t>(t) * k;
   for (int j0 = 0; j0 < k; j0 += 64) {
     const Slots<WEIGHTED> slots(pr, w + static_cast<size_t>(t) * k, j0, k, P);
@@ -29,7 +30,7 @@ __global__ __launch_bounds__(256) void k_dispatch(const void* x, const int32_t* 
     for (int u = 0; u < n; ++u) {
       const int r = slots.row(u);
       if (r < 0) continue;
-      const RowRef<A, false> row(rows, static_cast<size_t>(r) * H, H);
+      const Row row(rows, static_cast<size_t>(r) * H, H);
       if constexpr (WEIGHTED) {
         float f[V];
         A::unpack(v, f);
@@ -70,12 +71,12 @@ __device__ __forceinline__ void store_dots(const float* dots, float* dw, int k) 
 
 // A workgroup per token: the sum over its slots' rows and, with DW, each
 // row's dot product with x.
-template <class A, bool WEIGHTED, bool DW>
+template <class A, bool WEIGHTED, bool DW, bool STREAM>
 __global__ __launch_bounds__(1024) void k_dispatch_bwd(const void* drows, const int32_t* pair_row,
                                                        const float* w, const void* x,
                                                        const void* dx_in, void* dx, float* dw,
                                                        int H, int k, int P) {
-  typedef RowRef<A, false> Row;
+  typedef RowRef<A, false, STREAM> Row;
   constexpr int V = A::VEC;
   constexpr u32x4_t zero = {0u, 0u, 0u, 0u};
   extern __shared__ float dots[];
@@ -83,8 +84,8 @@ __global__ __launch_bounds__(1024) void k_dispatch_bwd(const void* drows, const 
   const size_t t = blockIdx.x;
   for (int i = 0; i * nt * V < H; ++i) {
     u32x4_t xr, ar;
-    if constexpr (DW) xr = Row(x, t * H, H).load(i, nt, tid);
-    ar = dx_in ? Row(dx_in, t * H, H).load(i, nt, tid) : zero;
+    if constexpr (DW) xr = Row(x, t * H, H).load_once(i, nt, tid);
+    ar = dx_in ? Row(dx_in, t * H, H).load_once(i, nt, tid) : zero;
     float acc[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
@@ -95,7 +96,7 @@ __global__ __launch_bounds__(1024) void k_dispatch_bwd(const void* drows, const 
       for (int q = 0; q < kSlotBatch; q += 4)
         if (j0 + q < k)
 #pragma unroll
-          for (int u = q; u < q + 4; ++u) v[u] = Row::slot(drows, slots.row(u), H).load(i, nt, tid);
+          for (int u = q; u < q + 4; ++u) v[u] = Row::slot(drows, slots.row(u), H).load_once(i, nt, tid);
 #pragma unroll
       for (int u = 0; u < kSlotBatch; ++u) {
         float dot = 0.f;
@@ -125,17 +126,17 @@ __global__ __launch_bounds__(1024) void k_dispatch_bwd(const void* drows, const 
 
 // A workgroup per token: its gradient row times the weight to each slot's
 // row and, with DW, the slots' dot products with it.
-template <class A, bool DW>
+template <class A, bool DW, bool STREAM>
 __global__ __launch_bounds__(1024) void k_combine_bwd(const void* dout, const void* y,
                                                       const int32_t* pair_row, const float* w,
                                                       void* dy, float* dw, int H, int k, int P) {
-  typedef RowRef<A, false> Row;
+  typedef RowRef<A, false, STREAM> Row;
   constexpr int V = A::VEC;
   extern __shared__ float dots[];
   const int nt = blockDim.x, tid = threadIdx.x;
   const size_t t = blockIdx.x;
   for (int i = 0; i * nt * V < H; ++i) {
-    const u32x4_t gr = Row(dout, t * H, H).load(i, nt, tid);
+    const u32x4_t gr = Row(dout, t * H, H).load_once(i, nt, tid);
     for (int j0 = 0; j0 < k; j0 += kSlotBatch) {
       u32x4_t v[kSlotBatch];
       const Slots<true> slots(pair_row + t * k, w + t * k, j0, k, P);
@@ -144,7 +145,7 @@ __global__ __launch_bounds__(1024) void k_combine_bwd(const void* dout, const vo
         for (int q = 0; q < kSlotBatch; q += 4)
           if (j0 + q < k)
 #pragma unroll
-            for (int u = q; u < q + 4; ++u) v[u] = Row::slot(y, slots.row(u), H).load(i, nt, tid);
+            for (int u = q; u < q + 4; ++u) v[u] = Row::slot(y, slots.row(u), H).load_once(i, nt, tid);
 #pragma unroll
       for (int u = 0; u < kSlotBatch; ++u) {
         float dot = 0.f;
@@ -233,15 +234,31 @@ static size_t dot_bytes(const moe_shape& s, int nt, const float* dw) {
   return dw ? static_cast<size_t>(s.top_k) * (nt / 64) * sizeof(float) : 0;
 }
 
+template <class A, bool STREAM>
+static auto dispatch_bwd_kernel(bool weighted, bool dw) {
+  return dw         ? k_dispatch_bwd<A, true, true, STREAM>
+         : weighted ? k_dispatch_bwd<A, true, false, STREAM>
+                    : k_dispatch_bwd<A, false, false, STREAM>;
+}
+
+template <class A, bool STREAM>
+static auto combine_bwd_kernel(bool dw) {
+  return dw ? k_combine_bwd<A, true, STREAM> : k_combine_bwd<A, false, STREAM>;
+}
+
+static bool streams_rows(const moe_shape& s) {
+  return streams_slots(static_cast<size_t>(s.T) * s.top_k * s.H * (s.act == MOE_DT_BF16 ? 2 : 4));
+}
+
 hipError_t launch_dispatch_bwd(const moe_shape& s, const void* drows, const int32_t* pair_row,
                                const float* w, const void* x, const void* dx_in, void* dx,
                                float* dw, hipStream_t st) {
   const int nt = token_threads(s);
-  const bool bf = s.act == MOE_DT_BF16;
-  auto kern = dw   ? (bf ? k_dispatch_bwd<RowBf16, true, true> : k_dispatch_bwd<RowF32, true, true>)
-              : w  ? (bf ? k_dispatch_bwd<RowBf16, true, false> : k_dispatch_bwd<RowF32, true, false>)
-              : bf ? k_dispatch_bwd<RowBf16, false, false>
-                   : k_dispatch_bwd<RowF32, false, false>;
+  const bool bf = s.act == MOE_DT_BF16, stream = streams_rows(s);
+  auto kern = bf ? (stream ? dispatch_bwd_kernel<RowBf16, true>(w, dw)
+                           : dispatch_bwd_kernel<RowBf16, false>(w, dw))
+                 : (stream ? dispatch_bwd_kernel<RowF32, true>(w, dw)
+                           : dispatch_bwd_kernel<RowF32, false>(w, dw));
   hipLaunchKernelGGL(kern, dim3(s.T), dim3(nt), dot_bytes(s, nt, dw), st, drows, pair_row, w, x,
                      dx_in, dx, dw, s.H, s.top_k, s.T * s.top_k);
   return hipGetLastError();
@@ -251,9 +268,11 @@ hipError_t launch_combine_bwd(const moe_shape& s, const void* dout, const void* 
                               const int32_t* pair_row, const float* w, void* dy, float* dw,
                               hipStream_t st) {
   const int nt = token_threads(s);
-  auto kern = s.act == MOE_DT_BF16
-                  ? (dw ? k_combine_bwd<RowBf16, true> : k_combine_bwd<RowBf16, false>)
-                  : (dw ? k_combine_bwd<RowF32, true> : k_combine_bwd<RowF32, false>);
+  const bool bf = s.act == MOE_DT_BF16, stream = streams_rows(s);
+  auto kern = bf ? (stream ? combine_bwd_kernel<RowBf16, true>(dw)
+                           : combine_bwd_kernel<RowBf16, false>(dw))
+                 : (stream ? combine_bwd_kernel<RowF32, true>(dw)
+                           : combine_bwd_kernel<RowF32, false>(dw));
   hipLaunchKernelGGL(kern, dim3(s.T), dim3(nt), dot_bytes(s, nt, dw), st, dout, y, pair_row, w, dy,
                      dw, s.H, s.top_k, s.T * s.top_k);
   return hipGetLastError();

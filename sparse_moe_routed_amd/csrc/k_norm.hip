@@ -19,9 +19,9 @@ struct FwdArgs {
 // (C of them).  WAVE: a wave per row, blockDim / 64 rows per workgroup, no
 // barrier; else a workgroup per row.  An absent matrix is held as zeros
 // (weights: offset 1), so that nothing but loads depends on it.
-template <class A, bool WAVE, int C, bool COMBINE, bool ODD, int GATE>
+template <class A, bool WAVE, int C, bool COMBINE, bool ODD, bool STREAM, int GATE>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
-  typedef RowRef<A, ODD> Row;
+  typedef RowRef<A, ODD, STREAM> Row;
   constexpr int V = A::VEC;
   __shared__ float red[WAVE ? 1 : 2][16];
   const int nt = WAVE ? 64 : blockDim.x;
@@ -33,15 +33,16 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
   const size_t o = static_cast<size_t>(t) * H;
   const uint32_t flags = p.n.flags;
   const bool normed = !(flags & MOE_N_NO_NORM);
-  auto load = [&](const void* m, size_t at, int i) { return Row(m, at, H).load(i, nt, tid); };
+  auto load = [&](const void* m, int i) { return Row(m, 0, H).load(i, nt, tid); };
+  auto load_once = [&](const void* m, int i) { return Row(m, o, H).load_once(i, nt, tid); };
   auto store = [&](void* m, int i, const float(&x)[V]) { Row(m, o, H).store(i, nt, tid, x); };
 
   // everything is requested before the first use where registers allow
   constexpr bool EARLY = WAVE || C <= 2;
   constexpr u32x4_t zero = {0u, 0u, 0u, 0u};
-  auto weight = [&](int i) { return normed ? load(p.a.w, 0, i) : zero; };
-  auto gate = [&](int i) { return load(p.a.gate, o, i); };
-  auto residual = [&](int i) { return p.a.residual ? load(p.a.residual, o, i) : zero; };
+  auto weight = [&](int i) { return normed ? load(p.a.w, i) : zero; };
+  auto gate = [&](int i) { return load_once(p.a.gate, i); };
+  auto residual = [&](int i) { return p.a.residual ? load_once(p.a.residual, i) : zero; };
   u32x4_t wr[EARLY ? C : 1], gr[EARLY ? C : 1], rr[EARLY ? C : 1], nr[EARLY ? C : 1];
   if constexpr (EARLY) {
 #pragma unroll
@@ -49,7 +50,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
       wr[i] = weight(i);
       if constexpr (GATE != kGateRow) gr[i] = gate(i);
       rr[i] = residual(i);
-      if (p.a.n_next) nr[i] = load(p.a.w_next, 0, i);
+      if (p.a.n_next) nr[i] = load(p.a.w_next, i);
     }
   }
   float v[C][V];
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
 #pragma unroll
           for (int u = q; u < q + G; ++u)
 #pragma unroll
-            for (int i = 0; i < C; ++i) y[u][i] = Row::slot(p.a.y, slots.row(u), H).load(i, nt, tid);
+            for (int i = 0; i < C; ++i) y[u][i] = Row::slot(p.a.y, slots.row(u), H).load_once(i, nt, tid);
 #pragma unroll
       for (int q = 0; q < KB; q += G)
         if (j0 + q < p.a.k)
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
       for (int i = 0; i < C; ++i) store(p.a.z_out, i, v[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < C; ++i) A::unpack(load(p.a.z, o, i), v[i]);
+    for (int i = 0; i < C; ++i) A::unpack(load_once(p.a.z, i), v[i]);
   }
   float gt = 1.f;
   if (flags & MOE_N_GATE_TOKEN) {
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     float f[V];
-    A::unpack(EARLY ? nr[i] : load(p.a.w_next, 0, i), f);
+    A::unpack(EARLY ? nr[i] : load(p.a.w_next, i), f);
 #pragma unroll
     for (int e = 0; e < V; ++e) v[i][e] *= rn * (f[e] + p.n.weight_offset);
     store(p.a.n_next, i, v[i]);
@@ -142,24 +143,25 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
 
 typedef void (*FwdKernel)(FwdArgs);
 
-template <bool ODD, int GATE>
+template <bool ODD, bool STREAM, int GATE>
 static FwdKernel fwd_wave(int C) {
   switch (C) {
-    case 1: return k_norm_fwd<RowBf16, true, 1, false, ODD, GATE>;
-    case 2: return k_norm_fwd<RowBf16, true, 2, false, ODD, GATE>;
-    case 3: return k_norm_fwd<RowBf16, true, 3, false, ODD, GATE>;
-    default: return k_norm_fwd<RowBf16, true, 5, false, ODD, GATE>;
+    case 1: return k_norm_fwd<RowBf16, true, 1, false, ODD, STREAM, GATE>;
+    case 2: return k_norm_fwd<RowBf16, true, 2, false, ODD, STREAM, GATE>;
+    case 3: return k_norm_fwd<RowBf16, true, 3, false, ODD, STREAM, GATE>;
+    default: return k_norm_fwd<RowBf16, true, 5, false, ODD, STREAM, GATE>;
   }
 }
 
-template <class A, bool COMBINE, bool ODD, int GATE>
+template <class A, bool COMBINE, bool ODD, bool STREAM, int GATE>
 static FwdKernel fwd_block(int C) {
   switch (C) {
-    case 1: return k_norm_fwd<A, false, 1, COMBINE, ODD, GATE>;
-    case 2: return k_norm_fwd<A, false, 2, COMBINE, ODD, GATE>;
-    case 4: return k_norm_fwd<A, false, 4, COMBINE, ODD, GATE>;
-    case 8: return k_norm_fwd<A, false, 8, COMBINE, ODD, GATE>;
-    default: return k_norm_fwd<A, false, 64 / A::VEC, COMBINE, ODD, GATE>;   // float32: 16
+    case 1: return k_norm_fwd<A, false, 1, COMBINE, ODD, STREAM, GATE>;
+    case 2: return k_norm_fwd<A, false, 2, COMBINE, ODD, STREAM, GATE>;
+    case 4: return k_norm_fwd<A, false, 4, COMBINE, ODD, STREAM, GATE>;
+    case 8: return k_norm_fwd<A, false, 8, COMBINE, ODD, STREAM, GATE>;
+    default:   // float32: 16
+      return k_norm_fwd<A, false, 64 / A::VEC, COMBINE, ODD, STREAM, GATE>;
   }
 }
 
@@ -167,6 +169,8 @@ template <class A, bool COMBINE, int GATE>
 static hipError_t fwd(const FwdArgs& p, hipStream_t st) {
   const int T = p.n.T, H = p.n.H, chunks = (H + A::VEC - 1) / A::VEC;
   const bool odd = H % A::VEC != 0;   // never with COMBINE: H % 128 == 0 there
+  const size_t row = H * sizeof(typename A::T);
+  const bool stream = COMBINE ? streams_slots(p.P * row) : streams_matrix(T * row);
   // A wave per row saves the barriers and is the faster one while there are
   // rows to fill the card with single waves and a row is at most 5 chunks per
   // lane; few rows finish sooner with a thread per chunk.  norm_out with a
@@ -177,7 +181,9 @@ static hipError_t fwd(const FwdArgs& p, hipStream_t st) {
   if constexpr (!COMBINE && A::VEC == 8) {
     if (T >= 1024 && chunks <= 5 * 64) {
       const int C = (chunks + 63) / 64;
-      auto kern = odd ? fwd_wave<true, GATE>(C) : fwd_wave<false, GATE>(C);
+      auto kern = odd      ? fwd_wave<true, false, GATE>(C)
+                  : stream ? fwd_wave<false, true, GATE>(C)
+                           : fwd_wave<false, false, GATE>(C);
       hipLaunchKernelGGL(kern, dim3((T + 3) / 4), dim3(256), 0, st, p);
       return hipGetLastError();
     }
@@ -185,7 +191,9 @@ static hipError_t fwd(const FwdArgs& p, hipStream_t st) {
   int C = 1;
   while (chunks > 1024 * C) C *= 2;
   const int nt = ((chunks + C - 1) / C + 63) / 64 * 64;
-  auto kern = odd ? fwd_block<A, COMBINE, !COMBINE, GATE>(C) : fwd_block<A, COMBINE, false, GATE>(C);
+  auto kern = odd      ? fwd_block<A, COMBINE, !COMBINE, false, GATE>(C)
+              : stream ? fwd_block<A, COMBINE, false, true, GATE>(C)
+                       : fwd_block<A, COMBINE, false, false, GATE>(C);
   hipLaunchKernelGGL(kern, dim3(T), dim3(nt), 0, st, p);
   return hipGetLastError();
 }

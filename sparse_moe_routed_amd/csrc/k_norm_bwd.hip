@@ -21,9 +21,9 @@ struct BwdArgs {
 // KEEP: the row stays in registers between the sums and the results
 // (otherwise it is read again, from the cache).  An absent matrix is held as
 // zeros (weights: offset 1), so that nothing but loads depends on it.
-template <class A, bool WAVE, int C, bool ODD, int GATE>
+template <class A, bool WAVE, int C, bool ODD, bool STREAM, int GATE>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
-  typedef RowRef<A, ODD> Row;
+  typedef RowRef<A, ODD, STREAM> Row;
   constexpr int V = A::VEC;
   constexpr bool KEEP = WAVE || C <= 2;
   __shared__ float2 red[2][WAVE ? 1 : 16];
@@ -37,7 +37,11 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
   const bool normed = !(flags & MOE_N_NO_NORM), sig = flags & MOE_N_GATE_SIGMOID;
   constexpr bool full = GATE != kGateRow;
   const float bs = p.n.branch_scale;
-  auto load = [&](const void* m, size_t at, int i) { return Row(m, at, H).load(i, nt, tid); };
+  // kept rows are read once; the others come back for the second pass
+  auto load = [&](const void* m, size_t at, int i) {
+    const Row row(m, at, H);
+    return KEEP ? row.load_once(i, nt, tid) : row.load(i, nt, tid);
+  };
   float acc[C][V];
 #pragma unroll
   for (int i = 0; i < C; ++i)
@@ -45,7 +49,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
     for (int e = 0; e < V; ++e) acc[i][e] = 0.f;
   constexpr u32x4_t zero = {0u, 0u, 0u, 0u};
   const float offset = normed ? p.n.weight_offset : 1.f;
-  auto load_w = [&](int i) { return normed ? load(p.a.w, 0, i) : zero; };
+  auto load_w = [&](int i) { return normed ? Row(p.a.w, 0, H).load(i, nt, tid) : zero; };
   auto load_s = [&](size_t o, int i) { return p.a.dres ? load(p.a.dres, o, i) : zero; };
   u32x4_t wr[KEEP ? C : 1];
   if constexpr (KEEP)
@@ -198,20 +202,20 @@ __global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part
 
 typedef void (*BwdKernel)(BwdArgs);
 
-template <class A, bool ODD, int GATE>
+template <class A, bool ODD, bool STREAM, int GATE>
 static BwdKernel bwd_kernel(bool wave, int C) {
   if (wave) switch (C) {
-      case 1: return k_norm_bwd<A, true, 1, ODD, GATE>;
-      case 2: return k_norm_bwd<A, true, 2, ODD, GATE>;
-      case 3: return k_norm_bwd<A, true, 3, ODD, GATE>;
-      default: return k_norm_bwd<A, true, 5, ODD, GATE>;
+      case 1: return k_norm_bwd<A, true, 1, ODD, STREAM, GATE>;
+      case 2: return k_norm_bwd<A, true, 2, ODD, STREAM, GATE>;
+      case 3: return k_norm_bwd<A, true, 3, ODD, STREAM, GATE>;
+      default: return k_norm_bwd<A, true, 5, ODD, STREAM, GATE>;
     }
   switch (C) {
-    case 1: return k_norm_bwd<A, false, 1, ODD, GATE>;
-    case 2: return k_norm_bwd<A, false, 2, ODD, GATE>;
-    case 4: return k_norm_bwd<A, false, 4, ODD, GATE>;
-    case 8: return k_norm_bwd<A, false, 8, ODD, GATE>;
-    default: return k_norm_bwd<A, false, 64 / A::VEC, ODD, GATE>;   // float32: 16
+    case 1: return k_norm_bwd<A, false, 1, ODD, STREAM, GATE>;
+    case 2: return k_norm_bwd<A, false, 2, ODD, STREAM, GATE>;
+    case 4: return k_norm_bwd<A, false, 4, ODD, STREAM, GATE>;
+    case 8: return k_norm_bwd<A, false, 8, ODD, STREAM, GATE>;
+    default: return k_norm_bwd<A, false, 64 / A::VEC, ODD, STREAM, GATE>;   // float32: 16
   }
 }
 
@@ -226,7 +230,10 @@ static void bwd(const BwdArgs& p, int G, hipStream_t st) {
     while (chunks > 1024 * C) C *= 2;
     nt = ((chunks + C - 1) / C + 63) / 64 * 64;
   }
-  auto kern = H % A::VEC ? bwd_kernel<A, true, GATE>(wave, C) : bwd_kernel<A, false, GATE>(wave, C);
+  const bool stream = streams_matrix(p.n.T * (H * sizeof(typename A::T)));
+  auto kern = H % A::VEC ? bwd_kernel<A, true, false, GATE>(wave, C)
+              : stream   ? bwd_kernel<A, false, true, GATE>(wave, C)
+                         : bwd_kernel<A, false, false, GATE>(wave, C);
   hipLaunchKernelGGL(kern, dim3(G), dim3(nt), wave && p.a.dw ? norm_part_pitch(H) * sizeof(float) : 0, st, p);
 }
 

@@ -137,6 +137,21 @@ hipError_t launch_zero_status(uint32_t* status, hipStream_t st);
 // sets `bit` in *status if any of the n values (bf16 or float32) is NaN/inf
 hipError_t launch_check_finite(const void* src, size_t n, bool bf16, uint32_t bit,
                                uint32_t* status, hipStream_t st);
+// Inputs that a call reads once bypass the caches (non-temporal) when they
+// could not stay there anyway; smaller ones may have just been written by the
+// call before.  Measured on pairs of calls that hand their output on, plain
+// against non-temporal loads, 2560 bf16:
+//   norm_out then norm_in gradient: matrices of 2.6 MB 8.9 / 9.4 us, 5.2 MB
+//   13.7 / 13.7, 7.9 MB 18.3 / 16.6, 21 MB 30.1 / 28.4, 84 MB 110 / 93 (a call
+//   has four or five matrices, the L2s hold 32 MB);
+//   dispatch, combine gradient, dispatch gradient, top-10: rows of 105 MB
+//   79 / 84 us, 157 MB 141 / 120, 210 MB 193 / 157 (two such matrices pass the
+//   256 MB cache in front of HBM).
+// Outputs are written through the caches at every size here: the next call
+// reads them (norm_out then norm_in gradient, 84 MB: 93 us against 100).
+constexpr bool streams_matrix(size_t bytes) { return bytes >= size_t{6} << 20; }
+constexpr bool streams_slots(size_t bytes) { return bytes >= size_t{128} << 20; }
+
 // The norms around the block.  Forward: z is a matrix, or (y, pair_row,
 // topk_w, k given) the combine of a token's slots; norm_in is the forward
 // kernel without gate, residual and next norm.

@@ -64,13 +64,15 @@ struct RowF32 {
 
 // One row of a matrix, read and written in 16-byte chunks: chunk i * nt + tid
 // by thread tid of nt.  Chunks past the row read as zeros and are not
-// written.  The row must be uniform over the wave.
+// written.  The row must be uniform over the wave.  load_once is for data
+// that this call reads once: with STREAM it does not stay in the caches
+// (when that pays: streams_matrix, streams_slots in moe_internal.h).
 //
 // ODD == false (H a multiple of VEC): a raw buffer of the row's bytes, whose
 // bounds check takes the place of a branch per chunk, with a scalar base and
 // one offset register for all chunks (wide rows otherwise held a 64-bit
 // address and a predicate per chunk and matrix, and spilled).
-template <class A, bool ODD>
+template <class A, bool ODD, bool STREAM>
 struct RowRef {
   typedef typename A::T T;
   static constexpr int V = A::VEC;
@@ -85,6 +87,9 @@ struct RowRef {
   }
   __device__ __forceinline__ u32x4_t load(int i, int nt, int tid) const {
     return __builtin_amdgcn_raw_buffer_load_b128(rs, tid * 16, i * nt * 16, 0);
+  }
+  __device__ __forceinline__ u32x4_t load_once(int i, int nt, int tid) const {
+    return __builtin_amdgcn_raw_buffer_load_b128(rs, tid * 16, i * nt * 16, STREAM ? 2 : 0);   // 2: nt
   }
   __device__ __forceinline__ void store(int i, int nt, int tid, const float (&v)[V]) const {
     store_raw(i, nt, tid, A::pack(v));
@@ -101,8 +106,8 @@ struct RowRef {
 
 // ODD: rows start at any element; the chunk that the row's end cuts is taken
 // element by element.
-template <class A>
-struct RowRef<A, true> {
+template <class A, bool STREAM>
+struct RowRef<A, true, STREAM> {
   typedef typename A::T T;
   static constexpr uint32_t V = A::VEC;
   T* row;
@@ -116,6 +121,9 @@ struct RowRef<A, true> {
 #pragma unroll
     for (uint32_t e = 0; e < V; ++e) v[e] = h + e < H ? A::get(row[h + e]) : 0.f;
     return A::pack(v);
+  }
+  __device__ __forceinline__ u32x4_t load_once(int i, int nt, int tid) const {
+    return load(i, nt, tid);
   }
   __device__ __forceinline__ void store(int i, int nt, int tid, const float (&v)[V]) const {
     const uint32_t h = static_cast<uint32_t>(i * nt + tid) * V;
