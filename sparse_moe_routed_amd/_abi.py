@@ -150,26 +150,34 @@ def ptr(t) -> int | None:
 
 
 _raw_stream = None
+_device = None
 
 
-def _current_stream():
-    """Function returning the handle of torch's current stream.  torch's
-    raw-stream query takes 0.3 us of host time, building a Stream object 2.8 us
-    (most of a small call)."""
+def _current_device() -> int:
+    """Index of torch's current device (its C query costs 0.1 us of host time
+    once CUDA is initialized, torch.cuda.current_device() three times that)."""
+    global _device
+    if _device is None:
+        import torch
+        torch.cuda.current_device()              # initializes
+        _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _device()
+
+
+def _current_stream() -> int:
+    """Handle of torch's current stream: its raw query takes 0.1 us, building a
+    Stream object 2.8 us (most of a small call's host time)."""
     global _raw_stream
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    device = torch.cuda.current_device
-    if raw is None:
-        _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
-    else:
-        _raw_stream = lambda: raw(device())
-    return _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(_current_device())
 
 
 def stream_handle(stream) -> int | None:
     if stream is None:
-        return (_raw_stream or _current_stream())()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -358,20 +366,21 @@ _TORCH = None
 
 
 def _torch_types():
-    """(act dtypes by moe_dtype, float32, int32, current device index function)"""
+    """(act dtypes by moe_dtype, float32, int32)"""
     global _TORCH
     if _TORCH is None:
         import torch
-        _TORCH = ((torch.float32, torch.bfloat16), torch.float32, torch.int32,
-                  torch.cuda.current_device)
+        _TORCH = ((torch.float32, torch.bfloat16), torch.float32, torch.int32)
     return _TORCH
 
 
-def _check_tensors(stream, args) -> int:
-    """Status of (tensor, dtype, elements) triples; addresses and None pass."""
-    device, memory = -2, 0
+def _pointers(stream, args):
+    """The addresses of (tensor, dtype, elements) triples, or a status if a
+    tensor is not what the call needs; addresses and None pass unchecked."""
+    device, memory, out = -2, 0, []
     for t, dtype, n in args:
         if t is None or type(t) is int:
+            out.append(t)
             continue
         if t.dtype is not dtype:
             return 3
@@ -380,13 +389,14 @@ def _check_tensors(stream, args) -> int:
         at = t.get_device()                     # -1: host memory
         if at != device:
             if device == -2 and at >= 0:
-                device = _torch_types()[3]()
+                device = _current_device()
             if at != device:
                 memory = 12
+        out.append(t.data_ptr())
     if stream is not None and device >= 0 and type(stream) is not int \
             and stream.device_index != device:
         memory = 12
-    return memory
+    return memory or out
 
 
 def _act_type(act):
@@ -396,15 +406,16 @@ def _act_type(act):
     return types[act] if 0 <= act < len(types) else None
 
 
-def _workspace_status(workspace, nbytes) -> int:
-    """A workspace tensor must hold nbytes on the current device."""
-    if workspace is None or isinstance(workspace, int):
-        return 0
+def _workspace(workspace, nbytes):
+    """The address of a workspace of at least nbytes on the current device, or
+    a status."""
+    if workspace is None or type(workspace) is int:
+        return workspace, 0
     if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
-        return 7
-    if not workspace.is_cuda or workspace.get_device() != _torch_types()[3]():
-        return 12
-    return 0
+        return None, 7
+    if workspace.get_device() < 0 or workspace.get_device() != _current_device():
+        return None, 12
+    return workspace.data_ptr(), 0
 
 
 def _gate_triple(norm, gate):
@@ -417,99 +428,83 @@ def moe_norm_workspace_size(norm) -> int:
     return int(load().moe_norm_workspace_size(ctypes.byref(norm)))
 
 
+def _call(name, head, stream, args, check, workspace=None, workspace_bytes=None) -> int:
+    """Entry point `name` on the structs `head`, the checked tensors `args`
+    (in the order of its C arguments) and, if it takes one, a workspace."""
+    p = _pointers(stream, args)
+    st = p if type(p) is int else 0
+    if not st and workspace_bytes is not None:
+        ws, st = _workspace(workspace, workspace_bytes)
+        p += (ws, workspace_bytes)
+    if not st:
+        st = getattr(_lib or load(), name)(*head, *p, stream_handle(stream))
+    return _ret(st, name, check)
+
+
 def moe_norm_in(norm, x, w, n, stream=None, check=True) -> int:
     a, m = _act_type(norm.act), norm.T * norm.H
-    st = _check_tensors(stream, ((x, a, m), (w, a, norm.H), (n, a, m)))
-    st = st or load().moe_norm_in(ctypes.byref(norm), ptr(x), ptr(w), ptr(n), stream_handle(stream))
-    return _ret(st, "moe_norm_in", check)
+    return _call("moe_norm_in", (norm,), stream, ((x, a, m), (w, a, norm.H), (n, a, m)), check)
 
 
 def moe_norm_in_backward(norm, dn, x, w, dres, dx, dw, workspace, workspace_bytes, stream=None,
                          check=True) -> int:
     a, m, H = _act_type(norm.act), norm.T * norm.H, norm.H
-    st = _check_tensors(stream, ((dn, a, m), (x, a, m), (w, a, H), (dres, a, m), (dx, a, m),
-                                 (dw, _torch_types()[1], H)))
-    st = st or _workspace_status(workspace, workspace_bytes)
-    st = st or load().moe_norm_in_backward(ctypes.byref(norm), ptr(dn), ptr(x), ptr(w), ptr(dres),
-                                           ptr(dx), ptr(dw), ptr(workspace), workspace_bytes,
-                                           stream_handle(stream))
-    return _ret(st, "moe_norm_in_backward", check)
+    return _call("moe_norm_in_backward", (norm,), stream,
+                 ((dn, a, m), (x, a, m), (w, a, H), (dres, a, m), (dx, a, m),
+                  (dw, _torch_types()[1], H)), check, workspace, workspace_bytes)
 
 
 def moe_norm_out(norm, z, w, gate, residual, w_next, out, n_next, stream=None, check=True) -> int:
     a, m, H = _act_type(norm.act), norm.T * norm.H, norm.H
-    st = _check_tensors(stream, ((z, a, m), (w, a, H), _gate_triple(norm, gate), (residual, a, m),
-                                 (w_next, a, H), (out, a, m), (n_next, a, m)))
-    st = st or load().moe_norm_out(ctypes.byref(norm), ptr(z), ptr(w), ptr(gate), ptr(residual),
-                                   ptr(w_next), ptr(out), ptr(n_next), stream_handle(stream))
-    return _ret(st, "moe_norm_out", check)
+    return _call("moe_norm_out", (norm,), stream,
+                 ((z, a, m), (w, a, H), _gate_triple(norm, gate), (residual, a, m), (w_next, a, H),
+                  (out, a, m), (n_next, a, m)), check)
 
 
 def moe_norm_out_backward(norm, dout, z, w, gate, dz, dgate, dw, workspace, workspace_bytes,
                           stream=None, check=True) -> int:
     a, m, H = _act_type(norm.act), norm.T * norm.H, norm.H
-    st = _check_tensors(stream, ((dout, a, m), (z, a, m), (w, a, H), _gate_triple(norm, gate),
-                                 (dz, a, m), _gate_triple(norm, dgate),
-                                 (dw, _torch_types()[1], H)))
-    st = st or _workspace_status(workspace, workspace_bytes)
-    st = st or load().moe_norm_out_backward(ctypes.byref(norm), ptr(dout), ptr(z), ptr(w),
-                                            ptr(gate), ptr(dz), ptr(dgate), ptr(dw),
-                                            ptr(workspace), workspace_bytes, stream_handle(stream))
-    return _ret(st, "moe_norm_out_backward", check)
+    return _call("moe_norm_out_backward", (norm,), stream,
+                 ((dout, a, m), (z, a, m), (w, a, H), _gate_triple(norm, gate), (dz, a, m),
+                  _gate_triple(norm, dgate), (dw, _torch_types()[1], H)), check, workspace,
+                 workspace_bytes)
 
 
 def moe_combine_norm(shape, norm, y, pair_row, topk_w, w, gate, residual, w_next, z, out, n_next,
                      stream=None, check=True) -> int:
-    a, f32, i32 = _act_type(norm.act), _torch_types()[1], _torch_types()[2]
+    a, (_, f32, i32) = _act_type(norm.act), _torch_types()
     m, H, P = norm.T * norm.H, norm.H, shape.T * shape.top_k
-    st = _check_tensors(stream, ((y, a, P * shape.H), (pair_row, i32, P), (topk_w, f32, P),
-                                 (w, a, H), _gate_triple(norm, gate), (residual, a, m),
-                                 (w_next, a, H), (z, a, m), (out, a, m), (n_next, a, m)))
-    st = st or load().moe_combine_norm(ctypes.byref(shape), ctypes.byref(norm), ptr(y),
-                                       ptr(pair_row), ptr(topk_w), ptr(w), ptr(gate),
-                                       ptr(residual), ptr(w_next), ptr(z), ptr(out), ptr(n_next),
-                                       stream_handle(stream))
-    return _ret(st, "moe_combine_norm", check)
+    return _call("moe_combine_norm", (shape, norm), stream,
+                 ((y, a, P * shape.H), (pair_row, i32, P), (topk_w, f32, P), (w, a, H),
+                  _gate_triple(norm, gate), (residual, a, m), (w_next, a, H), (z, a, m),
+                  (out, a, m), (n_next, a, m)), check)
 
 
 def moe_dispatch(shape, x, pair_row, topk_w, rows, stream=None, check=True) -> int:
-    a, f32, i32 = _act_type(shape.act), _torch_types()[1], _torch_types()[2]
-    P = shape.T * shape.top_k
-    st = _check_tensors(stream, ((x, a, shape.T * shape.H), (pair_row, i32, P), (topk_w, f32, P),
-                                 (rows, a, P * shape.H)))
-    st = st or load().moe_dispatch(ctypes.byref(shape), ptr(x), ptr(pair_row), ptr(topk_w),
-                                   ptr(rows), stream_handle(stream))
-    return _ret(st, "moe_dispatch", check)
+    a, (_, f32, i32), P = _act_type(shape.act), _torch_types(), shape.T * shape.top_k
+    return _call("moe_dispatch", (shape,), stream,
+                 ((x, a, shape.T * shape.H), (pair_row, i32, P), (topk_w, f32, P),
+                  (rows, a, P * shape.H)), check)
 
 
 def moe_dispatch_backward(shape, drows, pair_row, topk_w, x, dx_in, dx, dw, stream=None,
                           check=True) -> int:
-    a, f32, i32 = _act_type(shape.act), _torch_types()[1], _torch_types()[2]
-    P, m = shape.T * shape.top_k, shape.T * shape.H
-    st = _check_tensors(stream, ((drows, a, P * shape.H), (pair_row, i32, P), (topk_w, f32, P),
-                                 (x, a, m), (dx_in, a, m), (dx, a, m), (dw, f32, P)))
-    st = st or load().moe_dispatch_backward(ctypes.byref(shape), ptr(drows), ptr(pair_row),
-                                            ptr(topk_w), ptr(x), ptr(dx_in), ptr(dx), ptr(dw),
-                                            stream_handle(stream))
-    return _ret(st, "moe_dispatch_backward", check)
+    a, (_, f32, i32), P = _act_type(shape.act), _torch_types(), shape.T * shape.top_k
+    m = shape.T * shape.H
+    return _call("moe_dispatch_backward", (shape,), stream,
+                 ((drows, a, P * shape.H), (pair_row, i32, P), (topk_w, f32, P), (x, a, m),
+                  (dx_in, a, m), (dx, a, m), (dw, f32, P)), check)
 
 
 def moe_combine_backward(shape, dout, y, pair_row, topk_w, dy, dw, stream=None, check=True) -> int:
-    a, f32, i32 = _act_type(shape.act), _torch_types()[1], _torch_types()[2]
-    P = shape.T * shape.top_k
-    st = _check_tensors(stream, ((dout, a, shape.T * shape.H), (y, a, P * shape.H),
-                                 (pair_row, i32, P), (topk_w, f32, P), (dy, a, P * shape.H),
-                                 (dw, f32, P)))
-    st = st or load().moe_combine_backward(ctypes.byref(shape), ptr(dout), ptr(y), ptr(pair_row),
-                                           ptr(topk_w), ptr(dy), ptr(dw), stream_handle(stream))
-    return _ret(st, "moe_combine_backward", check)
+    a, (_, f32, i32), P = _act_type(shape.act), _torch_types(), shape.T * shape.top_k
+    return _call("moe_combine_backward", (shape,), stream,
+                 ((dout, a, shape.T * shape.H), (y, a, P * shape.H), (pair_row, i32, P),
+                  (topk_w, f32, P), (dy, a, P * shape.H), (dw, f32, P)), check)
 
 
 def moe_route_backward(shape, topk_ids, topk_w, dw, dlogits, stream=None, check=True) -> int:
-    f32, i32 = _torch_types()[1], _torch_types()[2]
-    P = shape.T * shape.top_k
-    st = _check_tensors(stream, ((topk_ids, i32, P), (topk_w, f32, P), (dw, f32, P),
-                                 (dlogits, f32, shape.T * shape.E)))
-    st = st or load().moe_route_backward(ctypes.byref(shape), ptr(topk_ids), ptr(topk_w), ptr(dw),
-                                         ptr(dlogits), stream_handle(stream))
-    return _ret(st, "moe_route_backward", check)
+    (_, f32, i32), P = _torch_types(), shape.T * shape.top_k
+    return _call("moe_route_backward", (shape,), stream,
+                 ((topk_ids, i32, P), (topk_w, f32, P), (dw, f32, P),
+                  (dlogits, f32, shape.T * shape.E)), check)

@@ -171,8 +171,14 @@ __global__ __launch_bounds__(1024) void k_combine_bwd(const void* dout, const vo
   if constexpr (DW) store_dots(dots, dw + t * k, k);
 }
 
-// A wave per token puts its row of dlogits together in LDS (only its own, so
-// no barrier: a wave's LDS operations stay in order).
+// Orders this wave's LDS accesses (they execute in program order; no other
+// wave shares the data, so no barrier).
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// A wave per token puts its row of dlogits together in LDS.
 __global__ __launch_bounds__(256) void k_route_bwd(const int32_t* __restrict__ ids,
                                                    const float* __restrict__ w,
                                                    const float* __restrict__ dw,
@@ -196,13 +202,13 @@ __global__ __launch_bounds__(256) void k_route_bwd(const int32_t* __restrict__ i
   float s = wj * dj;
   for (int j = lane + 64; j < k; j += 64) s = fmaf(w[t * k + j], dw[t * k + j], s);
   s = wave_sum_f32(s);
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_fence();
   if (id >= 0 && id < E) row[id] = wj * (dj - s);
   for (int j = lane + 64; j < k; j += 64) {
     const int e = ids[t * k + j];
     if (e >= 0 && e < E) row[e] = w[t * k + j] * (dw[t * k + j] - s);
   }
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_fence();
   float* out = dlogits + t * E;
   if (E % 4 == 0) {
     for (int e = lane; e < E / 4; e += 64) *reinterpret_cast<f32x4_t*>(out + 4 * e) = row4[e];

@@ -171,6 +171,8 @@ ROUTES = [  # T, H, E, k, drop
     (16, 256, 16, 2, 0.0), (33, 640, 60, 3, 0.5), (17, 1152, 40, 17, 0.0), (257, 128, 33, 7, 0.1),
     (40, 8192, 64, 8, 0.0), (5, 128, 1024, 130, 0.2), (700, 256, 512, 10, 0.0), (4, 65536, 8, 2, 0.0),
     (9, 512, 8, 4, 1.1),                      # every pair dropped
+    (1100, 4096, 64, 16, 0.1),                # rows past 128 MiB
+    (2, 8192, 1024, 1024, 0.1),               # every expert, 64 KB of LDS for the dot products
 ]
 RID = [f"{t}x{h}-{e}-{k}-{d}" for t, h, e, k, d in ROUTES]
 
@@ -542,6 +544,41 @@ def test_block_in_a_graph_repeats(act):
         got = b.outputs()
         for n in want:
             assert torch.equal(got[n], want[n]), (i, n)
+
+
+@pytest.mark.parametrize("T,H,E,I,k,tiled", [(8, 512, 64, 128, 6, True), (40, 256, 16, 64, 2, False)])
+def test_layer_buffers_block(T, H, E, I, k, tiled):
+    """MoELayerBuffers.block: norm, routed layer and residual have the bits of
+    moe_norm_in + moe_layer; the next block starts from its n_next."""
+    g, bf = Gen(T, H, 21), torch.bfloat16
+    buf = M.MoELayerBuffers(T, H, E, I, k, device=DEV, tiled=tiled)
+    wr = g(E, H, std=0.05, dtype=bf)
+    ws = [g(E, *sh, std=0.05, dtype=bf) for sh in ((I, H), (I, H), (H, I))]
+    ex = M.make_experts(*ws)
+    if tiled:
+        dst = [torch.empty_like(w) for w in ws]
+        M.moe_tile_experts(M.make_shape(T, H, E, I, k), ex, M.make_experts(*dst))
+        ex = M.make_experts(*dst)
+    w1, w2 = g(H, std=0.1, mean=1.0, dtype=bf), g(H, std=0.1, mean=1.0, dtype=bf)
+    x = g(T, H, dtype=bf)
+    pre, post = M.make_norm(T, H, eps=EPS), M.make_norm(T, H, eps=EPS, flags=NONORM)
+    n, out, n_next, ref = (Out(T, H, dtype=bf) for _ in range(4))
+    buf.block(x, pre, w1, wr, None, ex, post, None, residual=x, w_next=w2, n=n.t, out=out.t, n_next=n_next.t)
+    ids = buf.topk_ids.clone()
+    M.moe_norm_in(pre, x, w1, ref.t)
+    assert torch.equal(n.t, ref.t)
+    other = M.MoELayerBuffers(T, H, E, I, k, device=DEV, tiled=tiled)
+    other.layer(n.t, wr, None, ex, residual=x)
+    assert torch.equal(ids, other.topk_ids) and torch.equal(out.t, other.out)
+    # n_next is the norm of the sum before its rounding to out
+    v = out.t.double()
+    want, err = R._norm(v, v.abs() * R.u_of(bf), w2.double(), EPS)
+    R.check({"n": n_next.t}, {"n": (want, err + want.abs() * R.u_of(bf) + R.TINY)}, "n_next")
+    out2 = Out(T, H, dtype=bf)
+    buf.block(None, None, None, wr, None, ex, post, None, residual=out.t, n=n_next.t, out=out2.t)
+    other.layer(n_next.t, wr, None, ex, residual=out.t)
+    assert torch.equal(out2.t, other.out)
+    assert all(o.ok() for o in (n, out, n_next, ref, out2))
 
 
 def test_two_streams_at_once():
