@@ -187,9 +187,15 @@ __global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part
   const int col = threadIdx.x & 31, by = threadIdx.x >> 5;
   const int h = blockIdx.x * 32 + col;
   float s = 0.f;
-  if (h < H) {
-#pragma unroll 16
-    for (int g = by; g < G; g += 32) s += part[static_cast<size_t>(g) * pitch + h];
+  for (int g0 = by; g0 < G; g0 += 32 * 16) {
+    float v[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      const int g = g0 + 32 * u;
+      v[u] = g < G && h < H ? part[static_cast<size_t>(g) * pitch + h] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 16; ++u) s += v[u];
   }
   sum[by][col] = s;
   __syncthreads();

@@ -59,10 +59,14 @@ bool norm_bwd_wave(const moe_norm& n) {
   return n.T >= 2048 && n.H <= 320 * vec;
 }
 
-// Workgroups of the norm gradient: each leaves one row of column sums.
+// Workgroups of the norm gradient: each leaves one row of column sums, which
+// the second launch reads back.  Two per CU; a row each up to 256 rows, then
+// two rows or more (512 rows of 2560 bf16: 256 workgroups 8.4 us, 512 9.3;
+// 7168 bf16 14.1 / 16.5; at 1536 rows 512 workgroups are ahead, 13.6 / 15.7).
 int norm_bwd_groups(const moe_norm& n) {
-  const int rows = norm_bwd_wave(n) ? kNormWaves : 1;
-  return std::min((n.T + rows - 1) / rows, 512);
+  const int rows = norm_bwd_wave(n) ? (n.T + kNormWaves - 1) / kNormWaves
+                                    : std::max(std::min(n.T, 256), n.T / 2);
+  return std::min(rows, 512);
 }
 
 int locality_blocks(int T) {
