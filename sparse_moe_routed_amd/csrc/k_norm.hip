@@ -16,26 +16,31 @@ struct FwdArgs {
 };
 
 // Thread `tid` of the `nt` threads of a row holds chunks tid, tid + nt, ...
-// (C of them).  WAVE: a wave per row, blockDim / 64 rows per workgroup, no
-// barrier; else a workgroup per row.  An absent matrix is held as zeros
-// (weights: offset 1), so that nothing but loads depends on it.
-template <class A, bool WAVE, int C, bool COMBINE, bool ODD, bool STREAM, int GATE>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
-  typedef RowRef<A, ODD, STREAM> Row;
+// (C of them).  L: how threads share rows (RowShare); only a workgroup's row
+// needs barriers.  An absent matrix is held as zeros (weights: offset 1), so
+// that nothing but loads depends on it.
+template <class A, int L, int C, bool COMBINE, int EDGE, bool STREAM, int GATE>
+__global__ __launch_bounds__(L ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
+  typedef RowRef<A, EDGE == kEdgeOdd, STREAM> Row;
+  typedef RowShare<L> Share;
+  constexpr bool WAVE = Share::WAVE;
   constexpr int V = A::VEC;
   __shared__ float red[WAVE ? 1 : 2][16];
-  const int nt = WAVE ? 64 : blockDim.x;
-  const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
-  const int t = WAVE ? __builtin_amdgcn_readfirstlane(blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6))
-                     : blockIdx.x;
-  if (WAVE && t >= p.n.T) return;
-  const int H = p.n.H;
-  const size_t o = static_cast<size_t>(t) * H;
+  const int nt = Share::threads(), tid = Share::place();
+  const int t0 = WAVE ? __builtin_amdgcn_readfirstlane(
+                            (blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6)) * Share::ROWS)
+                      : blockIdx.x;
+  if (WAVE && t0 >= p.n.T) return;
+  const int t = t0 + Share::lane_row(), H = p.n.H;
   const uint32_t flags = p.n.flags;
   const bool normed = !(flags & MOE_N_NO_NORM);
   auto load = [&](const void* m, int i) { return Row(m, 0, H).load(i, nt, tid); };
-  auto load_once = [&](const void* m, int i) { return Row(m, o, H).load_once(i, nt, tid); };
-  auto store = [&](void* m, int i, const float(&x)[V]) { Row(m, o, H).store(i, nt, tid, x); };
+  auto load_once = [&](const void* m, int i) {
+    return row_ref<A, L, EDGE, STREAM>(m, t, p.n.T, H).load_once(i, nt, tid);
+  };
+  auto store = [&](void* m, int i, const float(&x)[V]) {
+    row_ref<A, L, EDGE, STREAM>(m, t, p.n.T, H).store(i, nt, tid, x);
+  };
 
   // everything is requested before the first use where registers allow
   constexpr bool EARLY = WAVE || C <= 2;
@@ -93,12 +98,16 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
 #pragma unroll
       for (int i = 0; i < C; ++i) store(p.a.z_out, i, v[i]);
   } else {
+    u32x4_t zr[C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) A::unpack(load_once(p.a.z, i), v[i]);
+    for (int i = 0; i < C; ++i) zr[i] = load_once(p.a.z, i);
+#pragma unroll
+    for (int i = 0; i < C; ++i) A::unpack(zr[i], v[i]);
   }
   float gt = 1.f;
   if (flags & MOE_N_GATE_TOKEN) {
-    gt = uniform_load(static_cast<const float*>(p.a.gate) + t);
+    const float* g = static_cast<const float*>(p.a.gate);
+    gt = Share::PACK ? (t < p.n.T ? g[t] : 0.f) : uniform_load(g + t0);
     if (flags & MOE_N_GATE_SIGMOID) gt = sigmoid<true>(gt);
   }
   float rs = 1.f;
@@ -108,7 +117,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
     for (int i = 0; i < C; ++i)
 #pragma unroll
       for (int e = 0; e < V; ++e) ss = fmaf(v[i][e], v[i][e], ss);
-    rs = rsqrtf(row_sum<WAVE>(ss, red[0]) / H + p.n.eps);
+    rs = rsqrtf(row_sum<L>(ss, red[0]) / H + p.n.eps);
   }
   const float offset = normed ? p.n.weight_offset : 1.f, factor = gt * p.n.branch_scale;
   float ss = 0.f;
@@ -130,7 +139,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
     store(p.a.out, i, v[i]);
   }
   if (!p.a.n_next) return;
-  const float rn = rsqrtf(row_sum<WAVE>(ss, red[WAVE ? 0 : 1]) / H + p.n.eps);
+  const float rn = rsqrtf(row_sum<L>(ss, red[WAVE ? 0 : 1]) / H + p.n.eps);
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     float f[V];
@@ -143,32 +152,43 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_fwd(FwdArgs p) {
 
 typedef void (*FwdKernel)(FwdArgs);
 
-template <bool ODD, bool STREAM, int GATE>
-static FwdKernel fwd_wave(int C) {
-  switch (C) {
-    case 1: return k_norm_fwd<RowBf16, true, 1, false, ODD, STREAM, GATE>;
-    case 2: return k_norm_fwd<RowBf16, true, 2, false, ODD, STREAM, GATE>;
-    case 3: return k_norm_fwd<RowBf16, true, 3, false, ODD, STREAM, GATE>;
-    default: return k_norm_fwd<RowBf16, true, 5, false, ODD, STREAM, GATE>;
+template <class A, int EDGE, bool STREAM, int GATE>
+static FwdKernel fwd_pack(int lanes) {
+  switch (lanes) {
+    case 8: return k_norm_fwd<A, 8, 1, false, EDGE, STREAM, GATE>;
+    case 16: return k_norm_fwd<A, 16, 1, false, EDGE, STREAM, GATE>;
+    default: return k_norm_fwd<A, 32, 1, false, EDGE, STREAM, GATE>;
   }
 }
 
-template <class A, bool COMBINE, bool ODD, bool STREAM, int GATE>
+template <int EDGE, bool STREAM, int GATE>
+static FwdKernel fwd_wave(int C) {
+  switch (C) {
+    case 1: return k_norm_fwd<RowBf16, 64, 1, false, EDGE, STREAM, GATE>;
+    case 2: return k_norm_fwd<RowBf16, 64, 2, false, EDGE, STREAM, GATE>;
+    case 3: return k_norm_fwd<RowBf16, 64, 3, false, EDGE, STREAM, GATE>;
+    default: return k_norm_fwd<RowBf16, 64, 5, false, EDGE, STREAM, GATE>;
+  }
+}
+
+template <class A, bool COMBINE, int EDGE, bool STREAM, int GATE>
 static FwdKernel fwd_block(int C) {
   switch (C) {
-    case 1: return k_norm_fwd<A, false, 1, COMBINE, ODD, STREAM, GATE>;
-    case 2: return k_norm_fwd<A, false, 2, COMBINE, ODD, STREAM, GATE>;
-    case 4: return k_norm_fwd<A, false, 4, COMBINE, ODD, STREAM, GATE>;
-    case 8: return k_norm_fwd<A, false, 8, COMBINE, ODD, STREAM, GATE>;
+    case 1: return k_norm_fwd<A, 0, 1, COMBINE, EDGE, STREAM, GATE>;
+    case 2: return k_norm_fwd<A, 0, 2, COMBINE, EDGE, STREAM, GATE>;
+    case 4: return k_norm_fwd<A, 0, 4, COMBINE, EDGE, STREAM, GATE>;
+    case 8: return k_norm_fwd<A, 0, 8, COMBINE, EDGE, STREAM, GATE>;
     default:   // float32: 16
-      return k_norm_fwd<A, false, 64 / A::VEC, COMBINE, ODD, STREAM, GATE>;
+      return k_norm_fwd<A, 0, 64 / A::VEC, COMBINE, EDGE, STREAM, GATE>;
   }
 }
 
 template <class A, bool COMBINE, int GATE>
 static hipError_t fwd(const FwdArgs& p, hipStream_t st) {
+  // bf16 rows of odd length have kernels of their own (H % 128 == 0 with COMBINE)
+  constexpr int ODD = A::VEC == 8 && !COMBINE ? kEdgeOdd : kEdgeWords;
   const int T = p.n.T, H = p.n.H, chunks = (H + A::VEC - 1) / A::VEC;
-  const bool odd = H % A::VEC != 0;   // never with COMBINE: H % 128 == 0 there
+  const bool odd = ODD == kEdgeOdd && H % 2 != 0;
   const size_t row = H * sizeof(typename A::T);
   const bool stream = COMBINE ? streams_slots(p.P * row) : streams_matrix(T * row);
   // A wave per row saves the barriers and is the faster one while there are
@@ -177,13 +197,23 @@ static hipError_t fwd(const FwdArgs& p, hipStream_t st) {
   // full gate, 2560 bf16: 1 row 4.4 us (wave) against 3.3 (workgroup), 512
   // rows 6.0 / 5.8, 2048 rows 12.7 / 13.8, 32768 rows 117 / 126.  float32
   // rows have twice the chunks: the workgroup is never slower there (4096 x
-  // 1024: 19.1 / 16.2 us).
+  // 1024: 19.1 / 16.2 us).  Rows of at most 32 chunks share a wave.
+  const int many = T >= 1024;
+  if (!COMBINE && many && chunks <= 32) {
+    const int lanes = norm_pack_lanes(chunks), rows = 4 * 64 / lanes;
+    auto kern = odd               ? fwd_pack<A, ODD, false, GATE>(lanes)
+                : H % A::VEC != 0 ? fwd_pack<A, kEdgeCut, false, GATE>(lanes)
+                : stream          ? fwd_pack<A, kEdgeWords, true, GATE>(lanes)
+                                  : fwd_pack<A, kEdgeWords, false, GATE>(lanes);
+    hipLaunchKernelGGL(kern, dim3((T + rows - 1) / rows), dim3(256), 0, st, p);
+    return hipGetLastError();
+  }
   if constexpr (!COMBINE && A::VEC == 8) {
-    if (T >= 1024 && chunks <= 5 * 64) {
+    if (many && chunks <= 5 * 64) {
       const int C = (chunks + 63) / 64;
-      auto kern = odd      ? fwd_wave<true, false, GATE>(C)
-                  : stream ? fwd_wave<false, true, GATE>(C)
-                           : fwd_wave<false, false, GATE>(C);
+      auto kern = odd      ? fwd_wave<ODD, false, GATE>(C)
+                  : stream ? fwd_wave<kEdgeWords, true, GATE>(C)
+                           : fwd_wave<kEdgeWords, false, GATE>(C);
       hipLaunchKernelGGL(kern, dim3((T + 3) / 4), dim3(256), 0, st, p);
       return hipGetLastError();
     }
@@ -191,9 +221,9 @@ static hipError_t fwd(const FwdArgs& p, hipStream_t st) {
   int C = 1;
   while (chunks > 1024 * C) C *= 2;
   const int nt = ((chunks + C - 1) / C + 63) / 64 * 64;
-  auto kern = odd      ? fwd_block<A, COMBINE, !COMBINE, false, GATE>(C)
-              : stream ? fwd_block<A, COMBINE, false, true, GATE>(C)
-                       : fwd_block<A, COMBINE, false, false, GATE>(C);
+  auto kern = odd      ? fwd_block<A, COMBINE, ODD, false, GATE>(C)
+              : stream ? fwd_block<A, COMBINE, kEdgeWords, true, GATE>(C)
+                       : fwd_block<A, COMBINE, kEdgeWords, false, GATE>(C);
   hipLaunchKernelGGL(kern, dim3(T), dim3(nt), 0, st, p);
   return hipGetLastError();
 }

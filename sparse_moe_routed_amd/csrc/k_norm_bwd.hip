@@ -17,19 +17,20 @@ struct BwdArgs {
   moe_norm n;
 };
 
-// WAVE: a wave per row, else a workgroup per row; rows t0, t0 + stride, ...
-// KEEP: the row stays in registers between the sums and the results
-// (otherwise it is read again, from the cache).  An absent matrix is held as
-// zeros (weights: offset 1), so that nothing but loads depends on it.
-template <class A, bool WAVE, int C, bool ODD, bool STREAM, int GATE>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
-  typedef RowRef<A, ODD, STREAM> Row;
+// L: how threads share rows (RowShare).  KEEP: the row stays in registers
+// between the sums and the results (otherwise it is read again, from the
+// cache).  An absent matrix is held as zeros (weights: offset 1), so that
+// nothing but loads depends on it.
+template <class A, int L, int C, int EDGE, bool STREAM, int GATE>
+__global__ __launch_bounds__(L ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
+  typedef RowRef<A, EDGE == kEdgeOdd, STREAM> Row;
+  typedef RowShare<L> Share;
+  constexpr bool WAVE = Share::WAVE;
   constexpr int V = A::VEC;
   constexpr bool KEEP = WAVE || C <= 2;
   __shared__ float2 red[2][WAVE ? 1 : 16];
   extern __shared__ float colsum[];   // WAVE: the workgroup's dw
-  const int nt = WAVE ? 64 : blockDim.x;
-  const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  const int nt = Share::threads(), tid = Share::place();
   const int wave = WAVE ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
   const int waves = WAVE ? blockDim.x >> 6 : 1;
   const int H = p.n.H;
@@ -38,8 +39,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
   constexpr bool full = GATE != kGateRow;
   const float bs = p.n.branch_scale;
   // kept rows are read once; the others come back for the second pass
-  auto load = [&](const void* m, size_t at, int i) {
-    const Row row(m, at, H);
+  auto load = [&](const void* m, int t, int i) {
+    const auto row = row_ref<A, L, EDGE, STREAM>(m, t, p.n.T, H);
     return KEEP ? row.load_once(i, nt, tid) : row.load(i, nt, tid);
   };
   float acc[C][V];
@@ -50,33 +51,35 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
   constexpr u32x4_t zero = {0u, 0u, 0u, 0u};
   const float offset = normed ? p.n.weight_offset : 1.f;
   auto load_w = [&](int i) { return normed ? Row(p.a.w, 0, H).load(i, nt, tid) : zero; };
-  auto load_s = [&](size_t o, int i) { return p.a.dres ? load(p.a.dres, o, i) : zero; };
+  auto load_s = [&](int t, int i) { return p.a.dres ? load(p.a.dres, t, i) : zero; };
   u32x4_t wr[KEEP ? C : 1];
   if constexpr (KEEP)
 #pragma unroll
     for (int i = 0; i < C; ++i) wr[i] = load_w(i);
   int parity = 0;
-  for (int t = blockIdx.x * waves + wave; t < p.n.T; t += gridDim.x * waves, parity ^= 1) {
-    const size_t o = static_cast<size_t>(t) * H;
+  const int step = gridDim.x * waves * Share::ROWS;
+  for (int t0 = (blockIdx.x * waves + wave) * Share::ROWS; t0 < p.n.T; t0 += step, parity ^= 1) {
+    const int t = t0 + Share::lane_row();
     u32x4_t zr[KEEP ? C : 1], dr[KEEP ? C : 1], gr[KEEP ? C : 1], sr[KEEP ? C : 1];
     if constexpr (KEEP)
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        zr[i] = load(p.a.z, o, i);
-        dr[i] = load(p.a.dout, o, i);
-        if constexpr (full) gr[i] = load(p.a.gate, o, i);
-        sr[i] = load_s(o, i);
+        zr[i] = load(p.a.z, t, i);
+        dr[i] = load(p.a.dout, t, i);
+        if constexpr (full) gr[i] = load(p.a.gate, t, i);
+        sr[i] = load_s(t, i);
       }
     float gt = 1.f;
     if (flags & MOE_N_GATE_TOKEN) {
-      gt = uniform_load(static_cast<const float*>(p.a.gate) + t);
+      const float* g = static_cast<const float*>(p.a.gate);
+      gt = Share::PACK ? (t < p.n.T ? g[t] : 0.f) : uniform_load(g + t0);
       if (sig) gt = sigmoid<true>(gt);
     }
     // the full gate's factors; a sigmoid is kept for the second use
     constexpr bool KEEP_G = KEEP && GATE == kGateFullSigmoid;
     float gk[KEEP_G ? C : 1][V];
     auto gate = [&](int i, float(&g)[V]) {
-      if constexpr (full) A::unpack(KEEP ? gr[i] : load(p.a.gate, o, i), g);
+      if constexpr (full) A::unpack(KEEP ? gr[i] : load(p.a.gate, t, i), g);
       if constexpr (GATE == kGateFullSigmoid)
 #pragma unroll
         for (int e = 0; e < V; ++e) g[e] = sigmoid<V == 4>(g[e]);
@@ -86,8 +89,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
     for (int i = 0; i < C; ++i) {
       if constexpr (!KEEP) asm volatile("" ::: "memory");   // keep the loads of a chunk together
       float z[V], d[V], w[V], g[V];
-      A::unpack(KEEP ? zr[i] : load(p.a.z, o, i), z);
-      A::unpack(KEEP ? dr[i] : load(p.a.dout, o, i), d);
+      A::unpack(KEEP ? zr[i] : load(p.a.z, t, i), z);
+      A::unpack(KEEP ? dr[i] : load(p.a.dout, t, i), d);
       A::unpack(KEEP ? wr[i] : load_w(i), w);
       gate(i, g);
       if constexpr (KEEP_G)
@@ -108,10 +111,10 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
         asm volatile("" : "+v"(zr[i]), "+v"(dr[i]), "+v"(wr[i]));
         if constexpr (full && !KEEP_G) asm volatile("" : "+v"(gr[i]));
       }
-    const float2 s = row_sum2<WAVE>(ss, s1, red[parity]);
+    const float2 s = row_sum2<L>(ss, s1, red[parity]);
     const float rs = normed ? rsqrtf(s.x / H + p.n.eps) : 1.f;
     s1 = bs * (rs * s.y);                                  // sum_h db zh (w) G_full
-    if ((flags & MOE_N_GATE_TOKEN) && p.a.dgate && tid == 0)
+    if ((flags & MOE_N_GATE_TOKEN) && p.a.dgate && tid == 0 && t < p.n.T)
       static_cast<float*>(p.a.dgate)[t] = s1 * (sig ? gt * (1.f - gt) : 1.f);
     const float c = normed ? gt * s1 / H : 0.f;            // mean(g zh)
     const float bg = bs * gt;
@@ -119,8 +122,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
     for (int i = 0; i < C; ++i) {
       if constexpr (!KEEP) asm volatile("" ::: "memory");
       float z[V], d[V], w[V], g[V], r[V];
-      A::unpack(KEEP ? zr[i] : load(p.a.z, o, i), z);
-      A::unpack(KEEP ? dr[i] : load(p.a.dout, o, i), d);
+      A::unpack(KEEP ? zr[i] : load(p.a.z, t, i), z);
+      A::unpack(KEEP ? dr[i] : load(p.a.dout, t, i), d);
       A::unpack(KEEP ? wr[i] : load_w(i), w);
       if constexpr (KEEP_G) {
 #pragma unroll
@@ -140,11 +143,11 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
             r[e] = bs * d[e] * z[e] * w[e];
             if constexpr (GATE == kGateFullSigmoid) r[e] *= g[e] * (1.f - g[e]);
           }
-          Row(p.a.dgate, o, H).store(i, nt, tid, r);
+          row_ref<A, L, EDGE, STREAM>(p.a.dgate, t, p.n.T, H).store(i, nt, tid, r);
         }
       }
       float sv[V];
-      A::unpack(KEEP ? sr[i] : load_s(o, i), sv);
+      A::unpack(KEEP ? sr[i] : load_s(t, i), sv);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         d[e] *= full ? bg * g[e] : bg;
@@ -152,16 +155,22 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
         r[e] = rs * fmaf(-z[e], c, d[e] * w[e]);
         r[e] = fmaf(p.n.residual_scale, sv[e], r[e]);
       }
-      Row(p.a.dz, o, H).store(i, nt, tid, r);
+      row_ref<A, L, EDGE, STREAM>(p.a.dz, t, p.n.T, H).store(i, nt, tid, r);
     }
   }
   if (!p.a.dw) return;
+  // the rows that share a wave
+  if constexpr (Share::PACK)
+#pragma unroll
+    for (int m = L; m < 64; m *= 2)
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[0][e] += wave_shfl_xor(acc[0][e], m);
   // rows of `part` and colsum are norm_part_pitch(H) long: whole chunks
   const int pitch = norm_part_pitch(H);
   float* part = p.a.part + static_cast<size_t>(blockIdx.x) * pitch;
   // WAVE: the waves add their sums in turn, the last one writes
   for (int k = 0; k < waves; ++k) {
-    if (k == wave)
+    if (k == wave && (!Share::PACK || Share::lane_row() == 0))
 #pragma unroll
       for (int i = 0; i < C; ++i)
 #pragma unroll
@@ -208,39 +217,52 @@ __global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part
 
 typedef void (*BwdKernel)(BwdArgs);
 
-template <class A, bool ODD, bool STREAM, int GATE>
-static BwdKernel bwd_kernel(bool wave, int C) {
-  if (wave) switch (C) {
-      case 1: return k_norm_bwd<A, true, 1, ODD, STREAM, GATE>;
-      case 2: return k_norm_bwd<A, true, 2, ODD, STREAM, GATE>;
-      case 3: return k_norm_bwd<A, true, 3, ODD, STREAM, GATE>;
-      default: return k_norm_bwd<A, true, 5, ODD, STREAM, GATE>;
+template <class A, int EDGE, bool STREAM, int GATE>
+static BwdKernel bwd_pack(int lanes) {
+  switch (lanes) {
+    case 8: return k_norm_bwd<A, 8, 1, EDGE, STREAM, GATE>;
+    case 16: return k_norm_bwd<A, 16, 1, EDGE, STREAM, GATE>;
+    default: return k_norm_bwd<A, 32, 1, EDGE, STREAM, GATE>;
+  }
+}
+
+template <class A, int EDGE, bool STREAM, int GATE>
+static BwdKernel bwd_kernel(int lanes, int C) {
+  if (lanes > 0 && lanes < 64) return bwd_pack<A, EDGE, STREAM, GATE>(lanes);
+  if (lanes == 64) switch (C) {
+      case 1: return k_norm_bwd<A, 64, 1, EDGE, STREAM, GATE>;
+      case 2: return k_norm_bwd<A, 64, 2, EDGE, STREAM, GATE>;
+      case 3: return k_norm_bwd<A, 64, 3, EDGE, STREAM, GATE>;
+      default: return k_norm_bwd<A, 64, 5, EDGE, STREAM, GATE>;
     }
   switch (C) {
-    case 1: return k_norm_bwd<A, false, 1, ODD, STREAM, GATE>;
-    case 2: return k_norm_bwd<A, false, 2, ODD, STREAM, GATE>;
-    case 4: return k_norm_bwd<A, false, 4, ODD, STREAM, GATE>;
-    case 8: return k_norm_bwd<A, false, 8, ODD, STREAM, GATE>;
-    default: return k_norm_bwd<A, false, 64 / A::VEC, ODD, STREAM, GATE>;   // float32: 16
+    case 1: return k_norm_bwd<A, 0, 1, EDGE, STREAM, GATE>;
+    case 2: return k_norm_bwd<A, 0, 2, EDGE, STREAM, GATE>;
+    case 4: return k_norm_bwd<A, 0, 4, EDGE, STREAM, GATE>;
+    case 8: return k_norm_bwd<A, 0, 8, EDGE, STREAM, GATE>;
+    default: return k_norm_bwd<A, 0, 64 / A::VEC, EDGE, STREAM, GATE>;   // float32: 16
   }
 }
 
 template <class A, int GATE>
 static void bwd(const BwdArgs& p, int G, hipStream_t st) {
   const int H = p.n.H, chunks = (H + A::VEC - 1) / A::VEC;
-  const bool wave = norm_bwd_wave(p.n);
+  const int lanes = norm_bwd_lanes(p.n);
   int C = 1, nt = 64 * kNormWaves;
-  if (wave) {
+  if (lanes) {
     C = (chunks + 63) / 64;
   } else {
     while (chunks > 1024 * C) C *= 2;
     nt = ((chunks + C - 1) / C + 63) / 64 * 64;
   }
   const bool stream = streams_matrix(p.n.T * (H * sizeof(typename A::T)));
-  auto kern = H % A::VEC ? bwd_kernel<A, true, false, GATE>(wave, C)
-              : stream   ? bwd_kernel<A, false, true, GATE>(wave, C)
-                         : bwd_kernel<A, false, false, GATE>(wave, C);
-  hipLaunchKernelGGL(kern, dim3(G), dim3(nt), wave && p.a.dw ? norm_part_pitch(H) * sizeof(float) : 0, st, p);
+  constexpr int ODD = A::VEC == 8 ? kEdgeOdd : kEdgeWords;
+  const bool pack = lanes > 0 && lanes < 64;
+  auto kern = A::VEC == 8 && H % 2      ? bwd_kernel<A, ODD, false, GATE>(lanes, C)
+              : pack && H % A::VEC != 0 ? bwd_pack<A, kEdgeCut, false, GATE>(lanes)
+              : stream                  ? bwd_kernel<A, kEdgeWords, true, GATE>(lanes, C)
+                                        : bwd_kernel<A, kEdgeWords, false, GATE>(lanes, C);
+  hipLaunchKernelGGL(kern, dim3(G), dim3(nt), lanes && p.a.dw ? norm_part_pitch(H) * sizeof(float) : 0, st, p);
 }
 
 template <class A>

@@ -49,14 +49,18 @@ bool tiles128_ok(const moe_shape& s) {
          s.I % 128 == 0;
 }
 
+int norm_pack_lanes(int chunks) { return chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunks <= 32 ? 32 : 64; }
+
 // A wave per row (up to 5 16-byte chunks per lane, with their column sums in
 // registers) once there are enough rows; few rows finish sooner with a
 // workgroup each, and longer rows need one.  2560 bf16, with dw: 1 row 8.5 us
 // (wave) against 4.8 (workgroup), 512 rows 11.1 / 9.5, 4096 rows 21.7 / 22.7,
 // 32768 rows 98 / 122; 256 bf16: 2048 rows 6.6 / 7.7.
-bool norm_bwd_wave(const moe_norm& n) {
-  const int vec = n.act == MOE_DT_BF16 ? 8 : 4;
-  return n.T >= 2048 && n.H <= 320 * vec;
+// Rows of at most 32 chunks share a wave.
+int norm_bwd_lanes(const moe_norm& n) {
+  const int vec = n.act == MOE_DT_BF16 ? 8 : 4, chunks = (n.H + vec - 1) / vec;
+  if (n.T < 2048 || chunks > 320) return 0;
+  return norm_pack_lanes(chunks);
 }
 
 // Workgroups of the norm gradient: each leaves one row of column sums, which
@@ -64,9 +68,11 @@ bool norm_bwd_wave(const moe_norm& n) {
 // two rows or more (512 rows of 2560 bf16: 256 workgroups 8.4 us, 512 9.3;
 // 7168 bf16 14.1 / 16.5; at 1536 rows 512 workgroups are ahead, 13.6 / 15.7).
 int norm_bwd_groups(const moe_norm& n) {
-  const int rows = norm_bwd_wave(n) ? (n.T + kNormWaves - 1) / kNormWaves
-                                    : std::max(std::min(n.T, 256), n.T / 2);
-  return std::min(rows, 512);
+  if (const int lanes = norm_bwd_lanes(n)) {
+    const int rows = kNormWaves * 64 / lanes;
+    return std::min((n.T + rows - 1) / rows, 512);
+  }
+  return std::min(std::max(std::min(n.T, 256), n.T / 2), 512);
 }
 
 int locality_blocks(int T) {

@@ -6,8 +6,8 @@
 
 namespace moe {
 
-// Chunks of rows whose length is no multiple of VEC start at any element:
-// global memory takes 16-byte accesses at element alignment.
+// Chunks of bf16 rows of odd length start at any element: global memory takes
+// 16-byte accesses at element alignment.
 typedef u32x4_t u32x4_e2 __attribute__((aligned(2)));
 
 // A value of an input at a wave-uniform address, through the scalar cache: no
@@ -68,10 +68,16 @@ struct RowF32 {
 // that this call reads once: with STREAM it does not stay in the caches
 // (when that pays: streams_matrix, streams_slots in moe_internal.h).
 //
-// ODD == false (H a multiple of VEC): a raw buffer of the row's bytes, whose
-// bounds check takes the place of a branch per chunk, with a scalar base and
-// one offset register for all chunks (wide rows otherwise held a 64-bit
-// address and a predicate per chunk and matrix, and spilled).
+// EDGE says what the end of a row does to its last chunk.
+constexpr int kEdgeWords = 0;   // whole chunks, or a cut that RowRef's bounds check handles
+constexpr int kEdgeCut = 1;     // a cut between words, rows sharing a wave (PackRef)
+constexpr int kEdgeOdd = 2;     // bf16 rows of odd length
+
+// kEdgeWords (rows are whole 32-bit words: float32, bf16 of even length): a
+// raw buffer of the row's bytes.  Its bounds check, word by word, takes the
+// place of a branch per chunk, also for a chunk that the row's end cuts, with
+// a scalar base and one offset register for all chunks (wide rows otherwise
+// held a 64-bit address and a predicate per chunk and matrix, and spilled).
 template <class A, bool ODD, bool STREAM>
 struct RowRef {
   typedef typename A::T T;
@@ -104,22 +110,24 @@ struct RowRef {
   }
 };
 
-// ODD: rows start at any element; the chunk that the row's end cuts is taken
-// element by element.
+// ODD: bf16 rows of odd length start at any element; the chunk that the row's
+// end cuts is taken element by element.
 template <class A, bool STREAM>
 struct RowRef<A, true, STREAM> {
   typedef typename A::T T;
   static constexpr uint32_t V = A::VEC;
   T* row;
   uint32_t H;
-  __device__ __forceinline__ RowRef(const void* m, size_t at, int len)
-      : row(const_cast<T*>(static_cast<const T*>(m)) + at), H(len) {}
+  bool on;
+  // `on`: the row exists (it may differ between lanes); H is uniform
+  __device__ __forceinline__ RowRef(const void* m, size_t at, int len, bool exists = true)
+      : row(const_cast<T*>(static_cast<const T*>(m)) + at), H(len), on(exists) {}
   __device__ __forceinline__ u32x4_t load(int i, int nt, int tid) const {
     const uint32_t h = static_cast<uint32_t>(i * nt + tid) * V;
-    if (h + V <= H) return *reinterpret_cast<const u32x4_e2*>(row + h);
+    if (on && h + V <= H) return *reinterpret_cast<const u32x4_e2*>(row + h);
     float v[V];
 #pragma unroll
-    for (uint32_t e = 0; e < V; ++e) v[e] = h + e < H ? A::get(row[h + e]) : 0.f;
+    for (uint32_t e = 0; e < V; ++e) v[e] = on && h + e < H ? A::get(row[h + e]) : 0.f;
     return A::pack(v);
   }
   __device__ __forceinline__ u32x4_t load_once(int i, int nt, int tid) const {
@@ -127,6 +135,7 @@ struct RowRef<A, true, STREAM> {
   }
   __device__ __forceinline__ void store(int i, int nt, int tid, const float (&v)[V]) const {
     const uint32_t h = static_cast<uint32_t>(i * nt + tid) * V;
+    if (!on) return;
     if (h + V <= H) {
       *reinterpret_cast<u32x4_e2*>(row + h) = A::pack(v);
     } else {
@@ -137,14 +146,96 @@ struct RowRef<A, true, STREAM> {
   }
 };
 
+// A row of at most 32 chunks whose wave holds several: chunk `tid` of row t, a
+// lane each, through a buffer of the whole matrix (of `rows` rows, under 2
+// GiB).  Lanes past the row or the matrix have an offset past its end.  CUT:
+// in the chunk that the row's end cuts, the next row's words are masked out
+// of loads and left out of stores (131072 x 128 bf16, norm gradient: 28.9 us
+// without the masks, 34.9 with them).
+template <class A, bool STREAM, bool CUT>
+struct PackRef {
+  typedef typename A::T T;
+  static constexpr int V = A::VEC;
+  static constexpr uint32_t kNowhere = 0x80000000u;
+  __amdgpu_buffer_rsrc_t rs;
+  uint32_t off;
+  int words;        // of this lane's chunk inside the row
+  int cut_words;    // of the cut chunk (uniform), 0 if there is none
+  __device__ __forceinline__ PackRef(const void* m, int t, int rows, int H, int tid)
+      : rs(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(m), 0,
+                                             rows * H * static_cast<int>(sizeof(T)), 0x00020000)) {
+    words = min(max(H - tid * V, 0), V) * static_cast<int>(sizeof(T)) / 4;
+    cut_words = H % V * static_cast<int>(sizeof(T)) / 4;
+    off = t < rows && words > 0 ? (t * H + tid * V) * static_cast<uint32_t>(sizeof(T)) : kNowhere;
+  }
+  template <int AUX>
+  __device__ __forceinline__ u32x4_t get() const {
+    u32x4_t r = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, AUX);
+    if constexpr (CUT)
+#pragma unroll
+      for (int e = 1; e < 4; ++e) r[e] = e < words ? r[e] : 0u;
+    return r;
+  }
+  __device__ __forceinline__ u32x4_t load(int, int, int) const { return get<0>(); }
+  __device__ __forceinline__ u32x4_t load_once(int, int, int) const { return get<STREAM ? 2 : 0>(); }
+  __device__ __forceinline__ void store(int, int, int, const float (&v)[V]) const {
+    const u32x4_t r = A::pack(v);
+    __builtin_amdgcn_raw_buffer_store_b128(r, rs, !CUT || words == 4 ? off : kNowhere, 0, 0);
+    if (!CUT) return;
+    const uint32_t cut = words < 4 ? off : kNowhere;
+    if (cut_words & 2) __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{r[0], r[1]}, rs, cut, 0, 0);
+    if (cut_words & 1)
+      __builtin_amdgcn_raw_buffer_store_b32(cut_words & 2 ? r[2] : r[0], rs,
+                                            cut + 4 * (cut_words & 2), 0, 0);
+  }
+};
+
+// How a row kernel's threads share rows.  L: lanes of a row; 0: the row is a
+// workgroup's, 64: a wave's, 8, 16 or 32: 64 / L rows share a wave.
+template <int L>
+struct RowShare {
+  static constexpr bool WAVE = L != 0, PACK = WAVE && L < 64;
+  static constexpr int ROWS = PACK ? 64 / L : 1;   // rows of a wave
+  // a row's threads and this thread's place among them
+  static __device__ __forceinline__ int threads() { return WAVE ? L : blockDim.x; }
+  static __device__ __forceinline__ int place() { return WAVE ? threadIdx.x % L : threadIdx.x; }
+  // this lane's row among the wave's
+  static __device__ __forceinline__ int lane_row() { return PACK ? (threadIdx.x & 63) / L : 0; }
+};
+
+// Row t of a matrix with `rows` rows.
+template <class A, int L, int EDGE, bool STREAM>
+__device__ __forceinline__ auto row_ref(const void* m, int t, int rows, int H) {
+  constexpr bool ODD = EDGE == kEdgeOdd;
+  if constexpr (RowShare<L>::PACK && !ODD)
+    return PackRef<A, STREAM, EDGE == kEdgeCut>(m, t, rows, H, RowShare<L>::place());
+  else if constexpr (RowShare<L>::PACK)
+    return RowRef<A, true, STREAM>(m, static_cast<size_t>(t) * H, H, t < rows);
+  else
+    return RowRef<A, ODD, STREAM>(m, static_cast<size_t>(t) * H, H);
+}
+
+// Sum over the L lanes (8 to 64) of each lane's row, in every one of them, in
+// a fixed association.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (L == 64) return wave_sum_f32(v);
+  v += __uint_as_float(dpp_u32<kDppXor1>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_u32<kDppXor2>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_u32<kDppHalfMirror>(__float_as_uint(v)));
+  if constexpr (L >= 16) v += __uint_as_float(dpp_u32<kDppMirror>(__float_as_uint(v)));
+  if constexpr (L >= 32) v += wave_shfl_xor(v, 16);
+  return v;
+}
+
 // Sums of one or two values per thread over the threads of a row, in a fixed
-// association, the results in every thread.  WAVE: the row is one wave; else
-// it is the whole workgroup, and `slot` is one float (2) per wave in LDS that
-// no other reduction uses until the next barrier after this one.
-template <bool WAVE>
+// association, the results in every thread.  A workgroup's row (L = 0) goes
+// through `slot`, one float (2) per wave in LDS that no other reduction uses
+// until the next barrier after this one.
+template <int L>
 __device__ __forceinline__ float row_sum(float v, float* slot) {
-  v = wave_sum_f32(v);
-  if constexpr (!WAVE) {
+  v = lanes_sum<L == 0 ? 64 : L>(v);
+  if constexpr (L == 0) {
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
     __syncthreads();
     v = slot[0];
@@ -153,10 +244,10 @@ __device__ __forceinline__ float row_sum(float v, float* slot) {
   return v;
 }
 
-template <bool WAVE>
+template <int L>
 __device__ __forceinline__ float2 row_sum2(float a, float b, float2* slot) {
-  float2 v = make_float2(wave_sum_f32(a), wave_sum_f32(b));
-  if constexpr (!WAVE) {
+  float2 v = make_float2(lanes_sum<L == 0 ? 64 : L>(a), lanes_sum<L == 0 ? 64 : L>(b));
+  if constexpr (L == 0) {
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
     __syncthreads();
     v = slot[0];

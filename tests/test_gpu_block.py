@@ -142,6 +142,38 @@ def test_norm_out_many_rows(T, H, flags, act):
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("flags", FLAGS)
+@pytest.mark.parametrize("T,H", [(2048, 1), (1025, 3), (2049, 7), (2063, 16), (2050, 31), (4099, 40), (2101, 64),
+                                 (2055, 65), (4097, 100), (2051, 128), (2049, 129), (2077, 250), (2049, 256),
+                                 (30001, 128), (50003, 64), (25001, 255)])
+def test_norm_out_rows_that_share_a_wave(T, H, flags, act):
+    run_norm_out(T, H, act, flags, nxt=T % 2 == 1, residual=H != 65)
+
+
+def test_special_values_stay_with_their_row_in_a_shared_wave():
+    T, H = 2050, 40
+    g = Gen(T, H)
+    for act in ("bf16", "f32"):
+        dt = DT[act]
+        x, w, dn = g(T, H, dtype=dt), g(H, std=0.1, mean=1.0, dtype=dt), g(T, H, dtype=dt)
+        bad = [3, 1029, 2049]
+        clean = x.clone()
+        for i, r in enumerate(bad):
+            x[r, i] = float("nan") if i else float("inf")
+        keep = [r for r in range(T) if r not in bad]
+        norm = M.make_norm(T, H, act, eps=EPS)
+        n, dx = Out(T, H, dtype=dt), Out(T, H, dtype=dt)
+        M.moe_norm_in(norm, x, w, n.t)
+        M.moe_norm_in_backward(norm, dn, x, w, None, dx.t, None, None, 0)
+        v, b = R.norm_in(clean, w, dtype=dt, eps=EPS, offset=0.0)["n"]
+        R.check({"n": n.t[keep]}, {"n": (v[keep], b[keep])}, "shared wave")
+        v, b = R.norm_bwd(dn, clean, w, None, None, dtype=dt, eps=EPS, offset=0.0, rscale=1.0, bscale=1.0,
+                          flags=0)["dz"]
+        R.check({"dz": dx.t[keep]}, {"dz": (v[keep], b[keep])}, "shared wave backward")
+        assert n.t[bad[1:]].isnan().all() and dx.t[bad[1:]].isnan().all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("H", [1, 5, 8, 63, 512, 513, 1537, 2049, 4100, 8192, 8201, 20480, 65535, 65536])
 def test_norm_out_widths(H, act):
     run_norm_out(4, H, act, FULL | SIG)
