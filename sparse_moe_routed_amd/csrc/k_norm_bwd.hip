@@ -5,6 +5,10 @@
 // float32 registers over the rows of a wave (or workgroup), then over the
 // waves of a workgroup in LDS, and a second launch adds the workgroups' rows
 // of partial sums: no atomics, the same bits every time.
+//
+// Bound by memory.  Measured (GPU time, then k_norm_dw): 32768 x 2560 bf16
+// with the residual path's gradient 127 + 4.6 us (5.3 TB/s of 671 MB), 4096 x
+// 2560 with a full sigmoid gate 24.3 + 4.6 us (4.3 TB/s of 105 MB).
 #include <algorithm>
 
 #include "moe_internal.h"
