@@ -1,4 +1,5 @@
-"""ctypes binding of libmoe.so: argument marshalling only.
+"""Binding of libmoe.so (ctypes; the calls around the layer: _block.so):
+argument marshalling only.
 
 Every function has the name of the C entry point it calls.  Tensor
 arguments may be torch tensors (their ``data_ptr()`` is passed), plain
@@ -350,10 +351,42 @@ def moe_stage_experts(shape, src, dst, perm, parts=None, stream=None, check=True
 
 
 # ---------------------------------------------------------------------------
-# The path around the routed experts.  Tensors given to these calls are also
-# checked here for what a bare pointer cannot tell: type (MOE_E_DTYPE), size
-# and dense layout (MOE_E_SHAPE), memory of the current device (MOE_E_MEMORY).
+# The path around the routed experts, through the compiled binding _block.so
+# (binding/block_binding.cpp): tensors given to these calls are also checked
+# for what a bare pointer cannot tell, type (MOE_E_DTYPE), size and dense
+# layout (MOE_E_SHAPE), memory of the current device (MOE_E_MEMORY).
 # ---------------------------------------------------------------------------
+
+_block = None
+_block_stream = None
+
+
+def _load_block():
+    """Import the binding (fails loudly when it has not been built)."""
+    global _block, _block_stream
+    load()
+    import torch                                 # the binding needs its libraries
+    if not os.path.exists(os.path.join(_PKG, "_block.so")):
+        raise RuntimeError("_block.so is missing: build it with `python -m sparse_moe_routed_amd.build`")
+    from . import _block as block
+    block.set_types(moe_shape, moe_norm)
+    # without a GPU the checks still answer
+    _block_stream = _current_stream if torch.cuda.is_available() else lambda: 0
+    _block = block
+    return block
+
+
+def _call(name, stream, check, *args) -> int:
+    block = _block or _load_block()
+    if stream is None:
+        handle = _block_stream()
+    elif isinstance(stream, int):
+        handle = stream
+    elif stream.device_index != _current_device():
+        return _ret(12, name, check)
+    else:
+        handle = stream.cuda_stream
+    return _ret(getattr(block, name)(*args, handle), name, check)
 
 
 def make_norm(T, H, act="bf16", eps=1e-6, weight_offset=0.0, residual_scale=1.0,
@@ -362,149 +395,49 @@ def make_norm(T, H, act="bf16", eps=1e-6, weight_offset=0.0, residual_scale=1.0,
                     branch_scale)
 
 
-_TORCH = None
-
-
-def _torch_types():
-    """(act dtypes by moe_dtype, float32, int32)"""
-    global _TORCH
-    if _TORCH is None:
-        import torch
-        _TORCH = ((torch.float32, torch.bfloat16), torch.float32, torch.int32)
-    return _TORCH
-
-
-def _pointers(stream, args):
-    """The addresses of (tensor, dtype, elements) triples, or a status if a
-    tensor is not what the call needs; addresses and None pass unchecked."""
-    device, memory, out = -2, 0, []
-    for t, dtype, n in args:
-        if t is None or type(t) is int:
-            out.append(t)
-            continue
-        if t.dtype is not dtype:
-            return 3
-        if t.numel() != n or not t.is_contiguous():
-            return 2
-        at = t.get_device()                     # -1: host memory
-        if at != device:
-            if device == -2 and at >= 0:
-                device = _current_device()
-            if at != device:
-                memory = 12
-        out.append(t.data_ptr())
-    if stream is not None and device >= 0 and type(stream) is not int \
-            and stream.device_index != device:
-        memory = 12
-    return memory or out
-
-
-def _act_type(act):
-    """The torch type of a moe_dtype (None, which no tensor has, for an
-    unknown one: the library reports that)."""
-    types = _torch_types()[0]
-    return types[act] if 0 <= act < len(types) else None
-
-
-def _workspace(workspace, nbytes):
-    """The address of a workspace of at least nbytes on the current device, or
-    a status."""
-    if workspace is None or type(workspace) is int:
-        return workspace, 0
-    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
-        return None, 7
-    if workspace.get_device() < 0 or workspace.get_device() != _current_device():
-        return None, 12
-    return workspace.data_ptr(), 0
-
-
-def _gate_triple(norm, gate):
-    if norm.flags & MOE_N_GATE_TOKEN:
-        return gate, _torch_types()[1], norm.T
-    return gate, _act_type(norm.act), norm.T * norm.H
-
-
 def moe_norm_workspace_size(norm) -> int:
     return int(load().moe_norm_workspace_size(ctypes.byref(norm)))
 
 
-def _call(name, head, stream, args, check, workspace=None, workspace_bytes=None) -> int:
-    """Entry point `name` on the structs `head`, the checked tensors `args`
-    (in the order of its C arguments) and, if it takes one, a workspace."""
-    p = _pointers(stream, args)
-    st = p if type(p) is int else 0
-    if not st and workspace_bytes is not None:
-        ws, st = _workspace(workspace, workspace_bytes)
-        p += (ws, workspace_bytes)
-    if not st:
-        st = getattr(_lib or load(), name)(*head, *p, stream_handle(stream))
-    return _ret(st, name, check)
-
-
 def moe_norm_in(norm, x, w, n, stream=None, check=True) -> int:
-    a, m = _act_type(norm.act), norm.T * norm.H
-    return _call("moe_norm_in", (norm,), stream, ((x, a, m), (w, a, norm.H), (n, a, m)), check)
+    return _call("moe_norm_in", stream, check, norm, x, w, n)
 
 
 def moe_norm_in_backward(norm, dn, x, w, dres, dx, dw, workspace, workspace_bytes, stream=None,
                          check=True) -> int:
-    a, m, H = _act_type(norm.act), norm.T * norm.H, norm.H
-    return _call("moe_norm_in_backward", (norm,), stream,
-                 ((dn, a, m), (x, a, m), (w, a, H), (dres, a, m), (dx, a, m),
-                  (dw, _torch_types()[1], H)), check, workspace, workspace_bytes)
+    return _call("moe_norm_in_backward", stream, check, norm, dn, x, w, dres, dx, dw, workspace,
+                 workspace_bytes)
 
 
 def moe_norm_out(norm, z, w, gate, residual, w_next, out, n_next, stream=None, check=True) -> int:
-    a, m, H = _act_type(norm.act), norm.T * norm.H, norm.H
-    return _call("moe_norm_out", (norm,), stream,
-                 ((z, a, m), (w, a, H), _gate_triple(norm, gate), (residual, a, m), (w_next, a, H),
-                  (out, a, m), (n_next, a, m)), check)
+    return _call("moe_norm_out", stream, check, norm, z, w, gate, residual, w_next, out, n_next)
 
 
 def moe_norm_out_backward(norm, dout, z, w, gate, dz, dgate, dw, workspace, workspace_bytes,
                           stream=None, check=True) -> int:
-    a, m, H = _act_type(norm.act), norm.T * norm.H, norm.H
-    return _call("moe_norm_out_backward", (norm,), stream,
-                 ((dout, a, m), (z, a, m), (w, a, H), _gate_triple(norm, gate), (dz, a, m),
-                  _gate_triple(norm, dgate), (dw, _torch_types()[1], H)), check, workspace,
-                 workspace_bytes)
+    return _call("moe_norm_out_backward", stream, check, norm, dout, z, w, gate, dz, dgate, dw,
+                 workspace, workspace_bytes)
 
 
 def moe_combine_norm(shape, norm, y, pair_row, topk_w, w, gate, residual, w_next, z, out, n_next,
                      stream=None, check=True) -> int:
-    a, (_, f32, i32) = _act_type(norm.act), _torch_types()
-    m, H, P = norm.T * norm.H, norm.H, shape.T * shape.top_k
-    return _call("moe_combine_norm", (shape, norm), stream,
-                 ((y, a, P * shape.H), (pair_row, i32, P), (topk_w, f32, P), (w, a, H),
-                  _gate_triple(norm, gate), (residual, a, m), (w_next, a, H), (z, a, m),
-                  (out, a, m), (n_next, a, m)), check)
+    return _call("moe_combine_norm", stream, check, shape, norm, y, pair_row, topk_w, w, gate,
+                 residual, w_next, z, out, n_next)
 
 
 def moe_dispatch(shape, x, pair_row, topk_w, rows, stream=None, check=True) -> int:
-    a, (_, f32, i32), P = _act_type(shape.act), _torch_types(), shape.T * shape.top_k
-    return _call("moe_dispatch", (shape,), stream,
-                 ((x, a, shape.T * shape.H), (pair_row, i32, P), (topk_w, f32, P),
-                  (rows, a, P * shape.H)), check)
+    return _call("moe_dispatch", stream, check, shape, x, pair_row, topk_w, rows)
 
 
 def moe_dispatch_backward(shape, drows, pair_row, topk_w, x, dx_in, dx, dw, stream=None,
                           check=True) -> int:
-    a, (_, f32, i32), P = _act_type(shape.act), _torch_types(), shape.T * shape.top_k
-    m = shape.T * shape.H
-    return _call("moe_dispatch_backward", (shape,), stream,
-                 ((drows, a, P * shape.H), (pair_row, i32, P), (topk_w, f32, P), (x, a, m),
-                  (dx_in, a, m), (dx, a, m), (dw, f32, P)), check)
+    return _call("moe_dispatch_backward", stream, check, shape, drows, pair_row, topk_w, x, dx_in,
+                 dx, dw)
 
 
 def moe_combine_backward(shape, dout, y, pair_row, topk_w, dy, dw, stream=None, check=True) -> int:
-    a, (_, f32, i32), P = _act_type(shape.act), _torch_types(), shape.T * shape.top_k
-    return _call("moe_combine_backward", (shape,), stream,
-                 ((dout, a, shape.T * shape.H), (y, a, P * shape.H), (pair_row, i32, P),
-                  (topk_w, f32, P), (dy, a, P * shape.H), (dw, f32, P)), check)
+    return _call("moe_combine_backward", stream, check, shape, dout, y, pair_row, topk_w, dy, dw)
 
 
 def moe_route_backward(shape, topk_ids, topk_w, dw, dlogits, stream=None, check=True) -> int:
-    (_, f32, i32), P = _torch_types(), shape.T * shape.top_k
-    return _call("moe_route_backward", (shape,), stream,
-                 ((topk_ids, i32, P), (topk_w, f32, P), (dw, f32, P),
-                  (dlogits, f32, shape.T * shape.E)), check)
+    return _call("moe_route_backward", stream, check, shape, topk_ids, topk_w, dw, dlogits)

@@ -1,4 +1,6 @@
-"""Compile the HIP kernels and the C-ABI layer into ``libmoe.so`` (gfx950).
+"""Compile the HIP kernels and the C-ABI layer into ``libmoe.so`` (gfx950),
+and the Python binding of the calls around the layer into ``_block.so`` (host
+code against torch's headers).
 
 Run ``python -m sparse_moe_routed_amd.build`` (or ``__graft_entry__.build()``).
 It always recompiles; objects go to ``_build/`` at the repository root.
@@ -10,12 +12,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
+BINDING = os.path.join(PKG, "_block.so")
 ARCH = "gfx950"
 
 # packed-fp32 instructions are disabled for all device code; MFMA results go
@@ -54,10 +58,41 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _run(cmd, what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed: {' '.join(cmd)}\n{r.stderr}")
+
+
+def _compile_binding() -> str:
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "block_binding.o")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
+          "-D__HIP_PLATFORM_AMD__", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I", os.path.join(ROOT, "include"), "-isystem", inc,
+          "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+          "-isystem", os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include"),
+          "-isystem", sysconfig.get_paths()["include"],
+          "-c", os.path.join(PKG, "binding", "block_binding.cpp"), "-o", obj], "binding compile")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    # libmoe.so beside it; torch and the HIP runtime are loaded by torch
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-lmoe", "-Wl,-rpath,$ORIGIN", "-L", lib,
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,--as-needed"], "binding link")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, srcs))
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
@@ -65,6 +100,7 @@ def build(verbose: bool = True) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding.result())
     if verbose:
         print(f"built {LIB}")
     return LIB

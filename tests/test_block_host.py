@@ -245,3 +245,24 @@ def test_tensors_are_checked():
     assert (out == 7).all()
     with pytest.raises(M.MoEError, match="moe_norm_in: MOE_E_SHAPE"):
         M.moe_norm_in(n, x[:3], w, out, stream=0)
+
+
+def test_binding_arguments():
+    """Arguments of the wrong kind raise; sizes whose product passes 64 bits
+    match no tensor; without a stream the checks still answer."""
+    x, w = torch.zeros(4, 96, dtype=torch.bfloat16), torch.zeros(96, dtype=torch.bfloat16)
+    for bad in (1.5, "x", [x]):
+        with pytest.raises(TypeError):
+            M.moe_norm_in(norm(), bad, w, x, stream=0)
+    for bad in (None, shape(), 16):
+        with pytest.raises(TypeError):
+            M.moe_norm_in(bad, x, w, x, stream=0)
+        with pytest.raises(TypeError):
+            M.moe_norm_in_backward(norm(), x, x, w, None, x, None, None, x, stream=0)
+    # 2^22 * 2^22 * 2^20 elements: 0 modulo 2^64
+    s = shape(T=1 << 22, top_k=1 << 22, H=1 << 20)
+    empty = torch.zeros(0, dtype=torch.bfloat16)
+    assert M.moe_combine_backward(s, None, empty, None, None, None, None, stream=0,
+                                  check=False) == SHAPE
+    assert M.moe_norm_in(norm(), x.float(), w, x, check=False) == DTYPE
+    assert M.moe_norm_in(norm(), x, w, x.clone(), check=False) == MEMORY
