@@ -232,10 +232,22 @@ hipError_t launch_dispatch(const moe_shape& s, const void* x, const int32_t* pai
   return hipGetLastError();
 }
 
-// Threads of a token's workgroup: one chunk each, up to 1024.
-static int token_threads(const moe_shape& s) {
-  const int chunks = s.H / (s.act == MOE_DT_BF16 ? 8 : 4);
-  return std::min((chunks + 63) / 64 * 64, 1024);
+// Threads of a token's workgroup: one chunk each, up to `most`; a longer row
+// takes rounds of as many.
+static int token_threads(const moe_shape& s, int most) {
+  const int chunks = s.H / (s.act == MOE_DT_BF16 ? 8 : 4), rounds = (chunks + most - 1) / most;
+  return ((chunks + rounds - 1) / rounds + 63) / 64 * 64;
+}
+
+// The dispatch gradient with dw holds the slots' rows until the dots are
+// summed, and one workgroup past 512 threads fills a CU.  Once there are more
+// tokens than CUs, two smaller ones hide each other's waits (top-8 bf16, up
+// to 1024 threads against 512: 512 x 7168 16.7 / 14.4 us, 1024 x 5120
+// 23.9 / 20.1, 2048 x 7168 65.0 / 58.1; 256 x 7168 9.5 / 10.4).  The combine
+// gradient and the plain sum gain nothing (2048 x 5504 83.8 / 88.8 and
+// 38.7 / 42.2).
+static int dispatch_bwd_threads(const moe_shape& s, const float* dw) {
+  return token_threads(s, dw && s.T > 256 ? 512 : 1024);
 }
 
 // LDS of the dot products (at most 1024 slots x 16 waves x 4 bytes = 64 KB).
@@ -262,7 +274,7 @@ static bool streams_rows(const moe_shape& s) {
 hipError_t launch_dispatch_bwd(const moe_shape& s, const void* drows, const int32_t* pair_row,
                                const float* w, const void* x, const void* dx_in, void* dx,
                                float* dw, hipStream_t st) {
-  const int nt = token_threads(s);
+  const int nt = dispatch_bwd_threads(s, dw);
   const bool bf = s.act == MOE_DT_BF16, stream = streams_rows(s);
   auto kern = bf ? (stream ? dispatch_bwd_kernel<RowBf16, true>(w, dw)
                            : dispatch_bwd_kernel<RowBf16, false>(w, dw))
@@ -276,7 +288,7 @@ hipError_t launch_dispatch_bwd(const moe_shape& s, const void* drows, const int3
 hipError_t launch_combine_bwd(const moe_shape& s, const void* dout, const void* y,
                               const int32_t* pair_row, const float* w, void* dy, float* dw,
                               hipStream_t st) {
-  const int nt = token_threads(s);
+  const int nt = token_threads(s, 1024);
   const bool bf = s.act == MOE_DT_BF16, stream = streams_rows(s);
   auto kern = bf ? (stream ? combine_bwd_kernel<RowBf16, true>(dw)
                            : combine_bwd_kernel<RowBf16, false>(dw))

@@ -26,7 +26,7 @@ struct BwdArgs {
 // cache).  An absent matrix is held as zeros (weights: offset 1), so that
 // nothing but loads depends on it.
 template <class A, int L, int C, int EDGE, bool STREAM, int GATE>
-__global__ __launch_bounds__(L ? 256 : 1024) void k_norm_bwd(BwdArgs p) {
+__global__ __launch_bounds__(!L ? 1024 : C == 1 ? 512 : 256) void k_norm_bwd(BwdArgs p) {
   typedef RowRef<A, EDGE == kEdgeOdd, STREAM> Row;
   typedef RowShare<L> Share;
   constexpr bool WAVE = Share::WAVE;
@@ -252,7 +252,7 @@ template <class A, int GATE>
 static void bwd(const BwdArgs& p, int G, hipStream_t st) {
   const int H = p.n.H, chunks = (H + A::VEC - 1) / A::VEC;
   const int lanes = norm_bwd_lanes(p.n);
-  int C = 1, nt = 64 * kNormWaves;
+  int C = 1, nt = 64 * norm_bwd_waves(p.n);
   if (lanes) {
     C = (chunks + 63) / 64;
   } else {

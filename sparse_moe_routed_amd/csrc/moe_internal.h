@@ -169,9 +169,9 @@ struct NormBwd {
   void *dz, *dgate;
   float *dw, *part;   // part: float [norm_bwd_groups][norm_part_pitch(H)]
 };
-constexpr int kNormWaves = 4;             // rows at a time of a gradient workgroup (wave per row)
 int norm_pack_lanes(int chunks);          // lanes of a row of that many chunks (8 .. 64)
 int norm_bwd_lanes(const moe_norm& n);    // lanes of a row in the gradient, 0: a workgroup
+int norm_bwd_waves(const moe_norm& n);    // waves of a gradient workgroup, if a row has lanes
 constexpr int norm_part_pitch(int H) { return (H + 7) / 8 * 8; }
 int norm_bwd_groups(const moe_norm& n);   // workgroups of the gradient kernel
 hipError_t launch_norm_fwd(const moe_norm& n, const NormFwd& a, hipStream_t st);

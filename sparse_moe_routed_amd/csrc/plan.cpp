@@ -63,13 +63,23 @@ int norm_bwd_lanes(const moe_norm& n) {
   return norm_pack_lanes(chunks);
 }
 
+// Four waves, two per SIMD at 512 workgroups; eight where a row is one chunk
+// per lane and each wave still gets four rows or more.  With the residual
+// path, four against eight: 131072 x 64 bf16 18.5 / 16.9 us, 32768 x 256
+// 18.5 / 17.2, 32768 x 384 28.1 / 24.8, 32768 x 333 67 / 44; with fewer rows
+// 8192 x 256 8.2 / 9.0, with two chunks per lane 16384 x 1024 28.3 / 29.7.
+int norm_bwd_waves(const moe_norm& n) {
+  const int vec = n.act == MOE_DT_BF16 ? 8 : 4, lanes = norm_bwd_lanes(n);
+  return lanes && n.H <= 64 * vec && n.T / (64 / lanes) >= 16384 ? 8 : 4;
+}
+
 // Workgroups of the norm gradient: each leaves one row of column sums, which
 // the second launch reads back.  Two per CU; a row each up to 256 rows, then
 // two rows or more (512 rows of 2560 bf16: 256 workgroups 8.4 us, 512 9.3;
 // 7168 bf16 14.1 / 16.5; at 1536 rows 512 workgroups are ahead, 13.6 / 15.7).
 int norm_bwd_groups(const moe_norm& n) {
   if (const int lanes = norm_bwd_lanes(n)) {
-    const int rows = kNormWaves * 64 / lanes;
+    const int rows = norm_bwd_waves(n) * 64 / lanes;
     return std::min((n.T + rows - 1) / rows, 512);
   }
   return std::min(std::max(std::min(n.T, 256), n.T / 2), 512);

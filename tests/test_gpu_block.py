@@ -150,6 +150,14 @@ def test_norm_out_rows_that_share_a_wave(T, H, flags, act):
     run_norm_out(T, H, act, flags, nxt=T % 2 == 1, residual=H != 65)
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("flags", [0, TOKEN, FULL | SIG])
+@pytest.mark.parametrize("T,H", [(131072, 13), (65537, 64), (32771, 250), (16384, 255), (16391, 333), (16385, 512)])
+def test_norm_out_eight_waves(T, H, flags, act):
+    """Rows enough for the gradient's larger workgroups."""
+    run_norm_out(T, H, act, flags, nxt=False, residual=False)
+
+
 def test_special_values_stay_with_their_row_in_a_shared_wave():
     T, H = 2050, 40
     g = Gen(T, H)
@@ -238,6 +246,20 @@ def test_dispatch(T, H, E, k, drop, act):
     dx2 = Out(T, H, dtype=dt)
     M.moe_dispatch_backward(s, drows, row, w, None, add, dx2.t, None)
     R.check({"dx": dx2.t}, R.dispatch_bwd(drows, row, w, x, add, T, dtype=dt, dw=False), "no dw")
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(256, 5504), (257, 4224), (300, 5504), (258, 7168), (261, 2176)])
+def test_dispatch_backward_in_rounds(T, H, act):
+    """Past 256 tokens a long row is a workgroup's work in rounds."""
+    k = 3
+    g, dt, s, _, w, row = case(T, H, 40, k, 0.1, act)
+    x, drows, dx_in = g(T, H, dtype=dt), g(T * k, H, std=0.5, dtype=dt), g(T, H, dtype=dt)
+    dx, dw = Out(T, H, dtype=dt), Out(T, k, dtype=torch.float32)
+    M.moe_dispatch_backward(s, drows, row, w, x, dx_in, dx.t, dw.t)
+    want = R.dispatch_bwd(drows, row, w, x, dx_in, T, dtype=dt, dw=True)
+    R.check({"dx": dx.t, "dw": dw.t}, want, "dispatch_backward")
+    assert dx.ok() and dw.ok()
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
