@@ -55,6 +55,13 @@ __global__ __launch_bounds__(!L ? 1024 : C == 1 ? 512 : 256) void k_norm_bwd(Bwd
   constexpr u32x4_t zero = {0u, 0u, 0u, 0u};
   const float offset = normed ? p.n.weight_offset : 1.f;
   auto load_w = [&](int i) { return normed ? Row(p.a.w, 0, H).load(i, nt, tid) : zero; };
+  // where neither a norm nor the gate's gradient wants z, its rows are taken
+  // as of no features: they read as zeros, without touching memory
+  const int Hz = normed || p.a.dgate ? H : 0;
+  auto load_z = [&](int t, int i) {
+    const auto row = row_ref<A, L, EDGE, STREAM>(p.a.z, t, p.n.T, Hz);
+    return KEEP ? row.load_once(i, nt, tid) : row.load(i, nt, tid);
+  };
   auto load_s = [&](int t, int i) { return p.a.dres ? load(p.a.dres, t, i) : zero; };
   u32x4_t wr[KEEP ? C : 1];
   if constexpr (KEEP)
@@ -68,7 +75,7 @@ __global__ __launch_bounds__(!L ? 1024 : C == 1 ? 512 : 256) void k_norm_bwd(Bwd
     if constexpr (KEEP)
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        zr[i] = load(p.a.z, t, i);
+        zr[i] = load_z(t, i);
         dr[i] = load(p.a.dout, t, i);
         if constexpr (full) gr[i] = load(p.a.gate, t, i);
         sr[i] = load_s(t, i);
@@ -93,7 +100,7 @@ __global__ __launch_bounds__(!L ? 1024 : C == 1 ? 512 : 256) void k_norm_bwd(Bwd
     for (int i = 0; i < C; ++i) {
       if constexpr (!KEEP) asm volatile("" ::: "memory");   // keep the loads of a chunk together
       float z[V], d[V], w[V], g[V];
-      A::unpack(KEEP ? zr[i] : load(p.a.z, t, i), z);
+      A::unpack(KEEP ? zr[i] : load_z(t, i), z);
       A::unpack(KEEP ? dr[i] : load(p.a.dout, t, i), d);
       A::unpack(KEEP ? wr[i] : load_w(i), w);
       gate(i, g);
@@ -126,7 +133,7 @@ __global__ __launch_bounds__(!L ? 1024 : C == 1 ? 512 : 256) void k_norm_bwd(Bwd
     for (int i = 0; i < C; ++i) {
       if constexpr (!KEEP) asm volatile("" ::: "memory");
       float z[V], d[V], w[V], g[V], r[V];
-      A::unpack(KEEP ? zr[i] : load(p.a.z, t, i), z);
+      A::unpack(KEEP ? zr[i] : load_z(t, i), z);
       A::unpack(KEEP ? dr[i] : load(p.a.dout, t, i), d);
       A::unpack(KEEP ? wr[i] : load_w(i), w);
       if constexpr (KEEP_G) {
@@ -156,7 +163,8 @@ __global__ __launch_bounds__(!L ? 1024 : C == 1 ? 512 : 256) void k_norm_bwd(Bwd
       for (int e = 0; e < V; ++e) {
         d[e] *= full ? bg * g[e] : bg;
         acc[i][e] = fmaf(d[e], z[e], acc[i][e]);
-        r[e] = rs * fmaf(-z[e], c, d[e] * w[e]);
+        r[e] = d[e] * w[e];
+        if (normed) r[e] = rs * fmaf(-z[e], c, r[e]);   // without a norm z may be infinite
         r[e] = fmaf(p.n.residual_scale, sv[e], r[e]);
       }
       row_ref<A, L, EDGE, STREAM>(p.a.dz, t, p.n.T, H).store(i, nt, tid, r);

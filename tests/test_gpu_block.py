@@ -363,6 +363,29 @@ def test_special_rows_stay_in_their_row(H, act):
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("flags", [0, TOKEN, FULL | SIG])
+@pytest.mark.parametrize("T,H", [(5, 40), (2050, 77), (2051, 2560), (3, 9000), (2, 33000)])
+def test_gradient_without_a_norm_does_not_hold_the_branch(T, H, flags, act):
+    """dz = G db: infinity and NaN in z reach the gate's gradient only."""
+    dt, g = DT[act], Gen(T, H, 7)
+    z, dout = g(T, H, dtype=dt), g(T, H, dtype=dt)
+    gate = g(T) if flags & TOKEN else g(T, H, dtype=dt) if flags else None
+    norm = M.make_norm(T, H, act, eps=EPS, branch_scale=1.25, flags=flags | NONORM)
+    v, b = R.norm_bwd(dout, z, None, gate, None, dtype=dt, eps=EPS, offset=0.0, rscale=1.0, bscale=1.25,
+                      flags=flags | NONORM)["dz"]
+    z[0, H // 2], z[1, H - 1] = float("inf"), float("nan")
+    for wanted in (True, False):
+        dz = Out(T, H, dtype=dt)
+        dg = Out(*gate.shape, dtype=gate.dtype) if wanted and flags else None
+        M.moe_norm_out_backward(norm, dout, z, None, gate, dz.t, dg.t if dg else None, None, None, 0)
+        R.check({"dz": dz.t}, {"dz": (v, b)}, "no norm")
+        assert dz.ok()
+        if dg:
+            bad = [0, 1] if flags & TOKEN else [(0, H // 2), (1, H - 1)]
+            assert not any(dg.t[i].isfinite() for i in bad) and dg.t[2:].isfinite().all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
 def test_dropped_pairs_are_not_read(act):
     """Rows that only a dropped pair would name may hold anything; a NaN in a
     kept row stays with its token."""
