@@ -53,9 +53,10 @@ int norm_pack_lanes(int chunks) { return chunks <= 8 ? 8 : chunks <= 16 ? 16 : c
 
 // A wave per row (up to 5 16-byte chunks per lane, with their column sums in
 // registers) once there are enough rows; few rows finish sooner with a
-// workgroup each, and longer rows need one.  2560 bf16, with dw: 1 row 8.5 us
-// (wave) against 4.8 (workgroup), 512 rows 11.1 / 9.5, 4096 rows 21.7 / 22.7,
-// 32768 rows 98 / 122; 256 bf16: 2048 rows 6.6 / 7.7.
+// workgroup each, and longer rows need one.  2560 bf16, with dw in
+// two launches: 1 row 8.5 us (wave) against 4.8 (workgroup), 512 rows 11.1 /
+// 9.5, 4096 rows 21.7 / 22.7, 32768 rows 98 / 122; 256 bf16: 2048 rows 6.6 /
+// 7.7.
 // Rows of at most 32 chunks share a wave.
 int norm_bwd_lanes(const moe_norm& n) {
   const int vec = n.act == MOE_DT_BF16 ? 8 : 4, chunks = (n.H + vec - 1) / vec;

@@ -188,6 +188,14 @@ def test_norm_out_widths(H, act):
     run_norm_out(3, H, act, TOKEN, grads=False)
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [1, 2, 6, 7, 333, 2560, 2563, 8194, 20485, 65535])
+def test_norm_out_single_row(H, act):
+    """One row is its own sum of columns."""
+    run_norm_out(1, H, act, FULL)
+    run_norm_out(1, H, act, TOKEN | SIG, nxt=False)
+
+
 # ---------------------------------------------------------------------------
 # Sorted rows
 # ---------------------------------------------------------------------------
