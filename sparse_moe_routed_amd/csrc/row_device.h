@@ -76,8 +76,10 @@ constexpr int kEdgeOdd = 2;     // bf16 rows of odd length
 // kEdgeWords (rows are whole 32-bit words: float32, bf16 of even length): a
 // raw buffer of the row's bytes.  Its bounds check, word by word, takes the
 // place of a branch per chunk, also for a chunk that the row's end cuts, with
-// a scalar base and one offset register for all chunks (wide rows otherwise
-// held a 64-bit address and a predicate per chunk and matrix, and spilled).
+// a scalar base for all chunks (wide rows otherwise held a 64-bit address and
+// a predicate per chunk and matrix, and spilled).  Every access carries its
+// whole offset in the vector register and the instruction: the check counts
+// those, not the scalar offset, and chunks past the row have to fail it.
 template <class A, bool ODD, bool STREAM>
 struct RowRef {
   typedef typename A::T T;
@@ -92,19 +94,19 @@ struct RowRef {
     return ref;
   }
   __device__ __forceinline__ u32x4_t load(int i, int nt, int tid) const {
-    return __builtin_amdgcn_raw_buffer_load_b128(rs, tid * 16, i * nt * 16, 0);
+    return __builtin_amdgcn_raw_buffer_load_b128(rs, (i * nt + tid) * 16, 0, 0);
   }
   __device__ __forceinline__ u32x4_t load_once(int i, int nt, int tid) const {
-    return __builtin_amdgcn_raw_buffer_load_b128(rs, tid * 16, i * nt * 16, STREAM ? 2 : 0);   // 2: nt
+    return __builtin_amdgcn_raw_buffer_load_b128(rs, (i * nt + tid) * 16, 0, STREAM ? 2 : 0);   // 2: nt
   }
   __device__ __forceinline__ void store(int i, int nt, int tid, const float (&v)[V]) const {
     store_raw(i, nt, tid, A::pack(v));
   }
-  // The whole offset goes into the vector register.  With a scalar offset the
-  // compiler puts no wait state between a 16-byte buffer store and the next
-  // instruction, and where that one overwrote the data registers, some lanes
-  // stored the new first word (seen now and then in 65536-wide float32 rows:
-  // values of chunk i + 1 in chunk i).
+  // A store has a second reason: with a scalar offset the compiler puts no
+  // wait state between a 16-byte buffer store and the next instruction, and
+  // where that one overwrote the data registers, some lanes stored the new
+  // first word (seen now and then in 65536-wide float32 rows: values of chunk
+  // i + 1 in chunk i).
   __device__ __forceinline__ void store_raw(int i, int nt, int tid, u32x4_t v) const {
     __builtin_amdgcn_raw_buffer_store_b128(v, rs, (i * nt + tid) * 16, 0, 0);
   }
