@@ -81,21 +81,23 @@ __global__ __launch_bounds__(!L ? 1024 : C == 1 ? 512 : 256) void k_norm_bwd(Bwd
         if constexpr (full) gr[i] = load(p.a.gate, t, i);
         sr[i] = load_s(t, i);
       }
+    // a token gate, or its sigmoid's tail, until the sums are there
     float gt = 1.f;
-    if (flags & MOE_N_GATE_TOKEN) {
+    if (!full && (flags & MOE_N_GATE_TOKEN)) {
       const float* g = static_cast<const float*>(p.a.gate);
       gt = Share::PACK ? (t < p.n.T ? g[t] : 0.f) : uniform_load(g + t0);
-      if (sig) gt = sigmoid<true>(gt);
+      if (sig) gt = sigmoid_tail<true>(gt);
     }
-    // the full gate's factors; a sigmoid is kept for the second use
+    // the full gate's factors; of a sigmoid its tail, kept for the second use
     constexpr bool KEEP_G = KEEP && GATE == kGateFullSigmoid;
     float gk[KEEP_G ? C : 1][V];
     auto gate = [&](int i, float(&g)[V]) {
       if constexpr (full) A::unpack(KEEP ? gr[i] : load(p.a.gate, t, i), g);
       if constexpr (GATE == kGateFullSigmoid)
 #pragma unroll
-        for (int e = 0; e < V; ++e) g[e] = sigmoid<V == 4>(g[e]);
+        for (int e = 0; e < V; ++e) g[e] = sigmoid_tail<V == 4>(g[e]);
     };
+    auto factor = [](float g) { return GATE == kGateFullSigmoid ? tail_sigmoid(g) : g; };
     float ss = 0.f, s1 = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -112,7 +114,7 @@ __global__ __launch_bounds__(!L ? 1024 : C == 1 ? 512 : 256) void k_norm_bwd(Bwd
       for (int e = 0; e < V; ++e) {
         const float dw = d[e] * (w[e] + offset);
         ss = fmaf(z[e], z[e], ss);
-        s1 = fmaf(full ? g[e] * dw : dw, z[e], s1);
+        s1 = fmaf(full ? factor(g[e]) * dw : dw, z[e], s1);
       }
     }
     // the row is unpacked again after the sums: twice the registers would be
@@ -122,12 +124,16 @@ __global__ __launch_bounds__(!L ? 1024 : C == 1 ? 512 : 256) void k_norm_bwd(Bwd
       for (int i = 0; i < C; ++i) {
         asm volatile("" : "+v"(zr[i]), "+v"(dr[i]), "+v"(wr[i]));
         if constexpr (full && !KEEP_G) asm volatile("" : "+v"(gr[i]));
+        if constexpr (KEEP_G)   // nor the factors beside their tails
+#pragma unroll
+          for (int e = 0; e < V; ++e) asm volatile("" : "+v"(gk[i][e]));
       }
     const float2 s = row_sum2<L>(ss, s1, red[parity]);
     const float rs = normed ? rsqrtf(s.x / H + p.n.eps) : 1.f;
     s1 = bs * (rs * s.y);                                  // sum_h db zh (w) G_full
-    if ((flags & MOE_N_GATE_TOKEN) && p.a.dgate && tid == 0 && t < p.n.T)
-      static_cast<float*>(p.a.dgate)[t] = s1 * (sig ? gt * (1.f - gt) : 1.f);
+    if (!full && (flags & MOE_N_GATE_TOKEN) && p.a.dgate && tid == 0 && t < p.n.T)
+      static_cast<float*>(p.a.dgate)[t] = s1 * (sig ? tail_slope(gt) : 1.f);
+    if (!full && sig) gt = tail_sigmoid(gt);
     const float c = normed ? gt * s1 / H : 0.f;            // mean(g zh)
     const float bg = bs * gt;
 #pragma unroll
@@ -153,7 +159,7 @@ __global__ __launch_bounds__(!L ? 1024 : C == 1 ? 512 : 256) void k_norm_bwd(Bwd
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             r[e] = bs * d[e] * z[e] * w[e];
-            if constexpr (GATE == kGateFullSigmoid) r[e] *= g[e] * (1.f - g[e]);
+            if constexpr (GATE == kGateFullSigmoid) r[e] *= tail_slope(g[e]);
           }
           row_ref<A, L, EDGE, STREAM>(p.a.dgate, t, p.n.T, H).store(i, nt, tid, r);
         }
@@ -162,7 +168,7 @@ __global__ __launch_bounds__(!L ? 1024 : C == 1 ? 512 : 256) void k_norm_bwd(Bwd
       A::unpack(KEEP ? sr[i] : load_s(t, i), sv);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        d[e] *= full ? bg * g[e] : bg;
+        d[e] *= full ? bg * factor(g[e]) : bg;
         acc[i][e] = fmaf(d[e], z[e], acc[i][e]);
         r[e] = d[e] * w[e];
         if (normed) r[e] = rs * fmaf(-z[e], c, r[e]);   // without a norm z may be infinite
