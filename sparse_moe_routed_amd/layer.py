@@ -118,7 +118,10 @@ class MoELayerBuffers:
         """One block around the routed experts: norm before, route, grouped
         FFN, then combine, norm after, gate, residual and the next block's
         norm in one launch.  n [T][H] receives the normed rows, or holds them
-        already (the previous block's n_next) when norm_in is None."""
+        already (the previous block's n_next) when norm_in is None.  A buffer
+        with check_finite is refused (MOE_E_FLAGS): these steps do not check."""
+        if self.shape.flags & _abi.MOE_F_CHECK_FINITE:
+            raise _abi.MoEError(10, "MoELayerBuffers.block with check_finite")
         if norm_in is not None:
             _abi.moe_norm_in(norm_in, x, w_in, n, stream)
         self.route_permute(n, w_router, bias, logits=False, stream=stream)
