@@ -40,3 +40,10 @@ def test_block_refuses_a_buffer_that_has_to_check(calls):
     with pytest.raises(M.MoEError, match="MOE_E_FLAGS") as e:
         block(M.MoELayerBuffers(T, H, E, I, K, device="cpu", check_finite=True))
     assert e.value.status == 10 and not calls
+
+
+@pytest.mark.parametrize("fused", [False, True])
+def test_block_runs_the_experts_its_buffer_asks_for(calls, fused):
+    block(M.MoELayerBuffers(T, H, E, I, K, device="cpu", tiled=True, fused=fused))
+    experts = ["moe_ffn_fused"] if fused else ["moe_ffn_gate_up", "moe_ffn_down"]
+    assert [n for n, _ in calls] == ["moe_norm_in", "moe_route_permute", *experts, "moe_combine_norm"]
