@@ -114,13 +114,14 @@ class MoELayerBuffers:
                                      self.out if out is None else out, n_next, stream)
 
     def block(self, x, norm_in, w_in, w_router, bias, experts, norm_out, w_out, gate=None,
-              residual=None, w_next=None, n=None, out=None, n_next=None, stream=None):
+              residual=None, w_next=None, n=None, out=None, n_next=None, stream=None, z=None):
         """One block around the routed experts: norm before, route, grouped
         FFN (moe_ffn_fused in a buffer made with fused), then combine, norm
         after, gate, residual and the next block's norm in one launch.  n
         [T][H] receives the normed rows, or holds them already (the previous
-        block's n_next) when norm_in is None.  A buffer with check_finite is
-        refused (MOE_E_FLAGS): these steps do not check."""
+        block's n_next) when norm_in is None; z [T][H], if given, the branch
+        before the norm after it, for moe_norm_out_backward.  A buffer with
+        check_finite is refused (MOE_E_FLAGS): these steps do not check."""
         if self.shape.flags & _abi.MOE_F_CHECK_FINITE:
             raise _abi.MoEError(10, "MoELayerBuffers.block with check_finite")
         if norm_in is not None:
@@ -131,7 +132,7 @@ class MoELayerBuffers:
         else:
             self.ffn_gate_up(n, experts, stream=stream)
             self.ffn_down(experts, stream=stream)
-        return self.combine_norm(norm_out, w_out, gate, residual, w_next, None, out, n_next,
+        return self.combine_norm(norm_out, w_out, gate, residual, w_next, z, out, n_next,
                                  stream=stream)
 
     def dispatch(self, x, rows, weighted=False, stream=None):

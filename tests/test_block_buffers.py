@@ -47,3 +47,15 @@ def test_block_runs_the_experts_its_buffer_asks_for(calls, fused):
     block(M.MoELayerBuffers(T, H, E, I, K, device="cpu", tiled=True, fused=fused))
     experts = ["moe_ffn_fused"] if fused else ["moe_ffn_gate_up", "moe_ffn_down"]
     assert [n for n, _ in calls] == ["moe_norm_in", "moe_route_permute", *experts, "moe_combine_norm"]
+
+
+def test_block_keeps_the_branch(calls):
+    """z, which the gradient of the norm after the block needs, reaches the
+    combine; without it nothing is written there."""
+    z = torch.zeros(T, H, dtype=torch.bfloat16)
+    for kept in (z, None):
+        calls.clear()
+        block(M.MoELayerBuffers(T, H, E, I, K, device="cpu"), z=kept)
+        name, args = calls[-1]
+        # shape, norm, y, pair_row, topk_w, w, gate, residual, w_next, z, ...
+        assert name == "moe_combine_norm" and args[9] is kept

@@ -32,3 +32,18 @@ def test_block_of_a_fused_buffer(T, H, E, I, k):
     other.combine_norm(post, w2, residual=x, out=ref.t)
     assert torch.equal(buf.y, other.y) and torch.equal(out.t, ref.t)
     assert out.t.isfinite().all() and n.ok() and out.ok()
+
+
+@pytest.mark.parametrize("fused", [False, True])
+def test_block_keeps_the_branch(fused):
+    """z is the combine's own result, and the other outputs do not change."""
+    T, H, E, I, k = 40, 256, 16, 128, 3
+    x, wr, ex, w1, w2, _keep = block_inputs(T, H, E, I)
+    pre, post = M.make_norm(T, H, eps=EPS), M.make_norm(T, H, eps=EPS)
+    n, out, ref, z = (Out(T, H, dtype=torch.bfloat16) for _ in range(4))
+    buf = M.MoELayerBuffers(T, H, E, I, k, device=DEV, tiled=True, fused=fused)
+    buf.block(x, pre, w1, wr, None, ex, post, w2, residual=x, n=n.t, out=ref.t)
+    buf.block(x, pre, w1, wr, None, ex, post, w2, residual=x, n=n.t, out=out.t, z=z.t)
+    assert torch.equal(out.t, ref.t)
+    buf.combine(out=ref.t)
+    assert torch.equal(z.t, ref.t) and all(o.ok() for o in (n, out, ref, z))
