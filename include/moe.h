@@ -489,7 +489,8 @@ int moe_norm_out(const moe_norm* norm, const void* z, const void* w, const void*
  *   sigmoid.
  * The residual's gradient is residual_scale * dout, which the next
  * moe_norm_in_backward adds as its dres.  dout, z, dz [T][H] act; dgate as
- * gate, or NULL; dw float [H] or NULL.  Gate, weight and their gradients
+ * gate, or NULL; dw float [H] or NULL.  z may be NULL where nothing depends
+ * on it (MOE_N_NO_NORM without dgate).  Gate, weight and their gradients
  * must match the flags (MOE_E_FLAGS: given without the flag; MOE_E_NULL:
  * flag without the gate). */
 int moe_norm_out_backward(const moe_norm* norm, const void* dout, const void* z, const void* w,

@@ -175,7 +175,9 @@ int moe_norm_out_backward(const moe_norm* norm, const void* dout, const void* z,
   const bool gated = (norm->flags & kGateBits) != 0, normed = !(norm->flags & MOE_N_NO_NORM);
   if ((!normed && dw) || (!gated && dgate)) return MOE_E_FLAGS;
   if (norm->T == 0) return empty_dw(*norm, dw, stream);
-  if ((st = check_ptrs({dout, z, dz}))) return st;
+  if ((st = check_ptrs({dout, dz}))) return st;
+  if ((normed || dgate) && !z) return MOE_E_NULL;   // else nothing reads it
+  if ((st = check_opt_ptr(z))) return st;
   if ((st = check_flagged(normed, w)) || (st = check_flagged(gated, gate))) return st;
   if ((st = check_opt_ptr(dgate)) || (st = check_opt_ptr(dw))) return st;
   if ((st = check_part(*norm, dw, workspace, workspace_bytes))) return st;

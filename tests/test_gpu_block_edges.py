@@ -6,7 +6,7 @@ import torch
 
 import sparse_moe_routed_amd as M
 from tests import block_ref as R
-from tests.test_gpu_block import DEV, DT, EPS, FLAGS, NONORM, Gen, Out, case, run_norm_out
+from tests.test_gpu_block import DEV, DT, EPS, FLAGS, FULL, NONORM, SIG, TOKEN, Gen, Out, case, run_norm_out
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +70,20 @@ def test_dropped_slots_read_nothing(H, bad, act):
     M.moe_dispatch_backward(s, y, row, None, None, dout, dx.t, None)
     R.check({"dx": dx.t}, R.dispatch_bwd(y, row, None, None, dout, T, dtype=dt, dw=False), "dispatch, no weights")
     assert all(o.ok() for o in (z, out, dy, dw, dx, dwt))
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("flags", [0, TOKEN, FULL, FULL | SIG])
+@pytest.mark.parametrize("T,H", [(1, 2560), (5, 77), (2050, 40), (2051, 33), (2051, 1999), (2048, 2560), (3, 9000),
+                                 (2, 40000)])
+def test_gradient_without_a_norm_needs_no_branch(T, H, flags, act):
+    """Without a norm and a gate's gradient nothing depends on z: NULL gives
+    the bits of any z."""
+    dt, g = DT[act], Gen(T, H, flags, 37)
+    dout, z = g(T, H, dtype=dt), g(T, H, dtype=dt)
+    gate = g(T) if flags & TOKEN else g(T, H, dtype=dt) if flags else None
+    norm = M.make_norm(T, H, act, branch_scale=1.25, flags=flags | NONORM)
+    a, b = Out(T, H, dtype=dt), Out(T, H, dtype=dt)
+    M.moe_norm_out_backward(norm, dout, z, None, gate, a.t, None, None, None, 0)
+    M.moe_norm_out_backward(norm, dout, None, None, gate, b.t, None, None, None, 0)
+    assert torch.equal(a.t, b.t) and a.t.isfinite().all() and a.ok() and b.ok()
