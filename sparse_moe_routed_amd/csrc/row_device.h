@@ -48,8 +48,6 @@ struct RowBf16 {
 struct RowF32 {
   typedef float T;
   static constexpr int VEC = 4;
-  static __device__ __forceinline__ float get(float v) { return v; }
-  static __device__ __forceinline__ float put(float v) { return v; }
   static __device__ __forceinline__ void unpack(u32x4_t r, float (&v)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
