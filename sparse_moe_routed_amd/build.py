@@ -1,6 +1,7 @@
 """Compile the HIP kernels and the C-ABI layer into ``libmoe.so`` (gfx950),
 and the Python binding of the calls around the layer into ``_block.so`` (host
-code against torch's headers).
+code against torch's headers).  The library needs hipcc only: without g++,
+Python's headers or torch it is built alone.
 
 Run ``python -m sparse_moe_routed_amd.build`` (or ``__graft_entry__.build()``).
 It always recompiles; objects go to ``_build/`` at the repository root.
@@ -64,44 +65,66 @@ def _run(cmd, what: str) -> None:
         raise RuntimeError(f"{what} failed: {' '.join(cmd)}\n{r.stderr}")
 
 
+def _binding_lacks() -> str | None:
+    """What is not there to build the binding with, if anything."""
+    if not shutil.which("g++"):
+        return "g++"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    try:
+        import torch
+    except ImportError:
+        return "torch"
+    header = os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc", "autograd",
+                          "python_variable.h")
+    return None if os.path.exists(header) else "torch's headers"
+
+
 def _compile_binding() -> str:
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
     obj = os.path.join(BUILD, "block_binding.o")
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
           "-D__HIP_PLATFORM_AMD__", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           "-I", os.path.join(ROOT, "include"), "-isystem", inc,
           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
-          "-isystem", os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include"),
+          "-isystem", os.path.join(rocm, "include"),
           "-isystem", sysconfig.get_paths()["include"],
           "-c", os.path.join(PKG, "binding", "block_binding.cpp"), "-o", obj], "binding compile")
     return obj
 
 
-def _link_binding(obj: str) -> None:
+def _link_binding(obj: str, lib: str, out: str) -> None:
     import torch
-    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = BINDING + ".tmp"
-    # libmoe.so beside it; torch and the HIP runtime are loaded by torch
-    _run(["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-lmoe", "-Wl,-rpath,$ORIGIN", "-L", lib,
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    # libmoe.so (its soname) beside it; torch and the HIP runtime are loaded by torch
+    _run(["g++", "-shared", "-o", out, obj, lib, "-Wl,-rpath,$ORIGIN", "-L", libs,
           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,--as-needed"], "binding link")
-    os.replace(tmp, BINDING)
 
 
 def build(verbose: bool = True) -> str:
+    """Both files are replaced once both are linked: a build that fails leaves
+    the older pair, and a library is never left beside a binding of another."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
+    lacks = _binding_lacks()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = None if lacks else ex.submit(_compile_binding)
         objs = list(ex.map(_compile, srcs))
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libmoe.so", "-o", tmp,
-           *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_binding(binding.result())
+    lib, block = LIB + ".tmp", BINDING + ".tmp"
+    _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libmoe.so", "-o", lib, *objs],
+         "link")
+    if binding:
+        _link_binding(binding.result(), lib, block)
+    if os.path.exists(BINDING):
+        os.remove(BINDING)
+    os.replace(lib, LIB)
+    if binding:
+        os.replace(block, BINDING)
+    else:
+        sys.stderr.write(f"{os.path.basename(BINDING)} was not built, {lacks} is missing: the calls around "
+                         "the layer have no Python binding\n")
     if verbose:
         print(f"built {LIB}")
     return LIB
