@@ -294,11 +294,10 @@ def _own_buffers(s):
                  dw=new(H, dtype=torch.float32) if c["post"] else None,
                  dgate=None if s["gate"] is None else torch.empty_like(s["gate"]))
     elif kind == "dispatch":
-        s.update(rows=torch.zeros((P, H), dtype=dt, device=_DEV), dx=new(T, H),
+        s.update(rows=new(P, H), dx=new(T, H),
                  dw=new(T, c["k"], dtype=torch.float32) if c["weighted"] else None)
     else:
-        s.update(dy=torch.zeros((P, H), dtype=dt, device=_DEV),
-                 dw=new(T, c["k"], dtype=torch.float32),
+        s.update(dy=new(P, H), dw=new(T, c["k"], dtype=torch.float32),
                  dlogits=new(T, c["E"], dtype=torch.float32))
 
 
@@ -346,6 +345,8 @@ def _run_own(s):
     elif kind == "dispatch":
         w = s["topk_w"] if c["weighted"] else None
         if c["direction"] != "bwd":
+            if c["drop"]:
+                s["rows"].zero_()              # rows that no pair names
             M.moe_dispatch(s["shape"], s["x"], s["pair_row"], w, s["rows"])
             res["rows"] = s["rows"]
         if c["direction"] != "fwd":
@@ -355,6 +356,8 @@ def _run_own(s):
             if c["weighted"]:
                 res["dw"] = s["dw"]
     else:
+        if c["drop"]:
+            s["dy"].zero_()                    # rows that no pair names
         M.moe_combine_backward(s["shape"], s["dout"], s["y"], s["pair_row"], s["topk_w"], s["dy"],
                                s["dw"])
         M.moe_route_backward(s["shape"], s["topk_ids"], s["topk_w"], s["dw"], s["dlogits"])
