@@ -2,9 +2,9 @@
 // route weights (formulas: include/moe.h).  Bound by memory: every row is
 // read and written once, in 16-byte chunks, and the T tokens are the unit of
 // work, so that a token's own row is read once for its k slots.
-// Measured, 4096 x 2560 bf16 top-10 (GPU time): dispatch 44.8 us (5.2 TB/s of
-// 231 MB), weighted dispatch gradient 50.7 us (5.0 TB/s of 252 MB), combine
-// gradient 88.9 us (5.0 TB/s of 441 MB), route gradient 5.6 us (latency).
+// Measured, 4096 x 2560 bf16 top-10 (GPU time): dispatch 44.3 us (5.2 TB/s of
+// 231 MB), weighted dispatch gradient 50.8 us (5.0 TB/s of 252 MB), combine
+// gradient 91.2 us (4.8 TB/s of 441 MB), route gradient 5.5 us (latency).
 #include <algorithm>
 
 #include "moe_internal.h"

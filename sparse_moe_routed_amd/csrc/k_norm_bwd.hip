@@ -8,8 +8,8 @@
 // own dw (1 x 2560 bf16 5.8 -> 3.2 us on the GPU without the second launch).
 //
 // Bound by memory.  Measured (GPU time, then k_norm_dw): 32768 x 2560 bf16
-// with the residual path's gradient 127 + 4.6 us (5.3 TB/s of 671 MB), 4096 x
-// 2560 with a full sigmoid gate 24.3 + 4.6 us (4.3 TB/s of 105 MB).
+// with the residual path's gradient 128 + 4.8 us (5.2 TB/s of 671 MB), 4096 x
+// 2560 with a full sigmoid gate 25.4 + 4.8 us (4.1 TB/s of 105 MB).
 #include <algorithm>
 
 #include "moe_internal.h"

@@ -111,7 +111,9 @@ struct RowRef {
 };
 
 // ODD: bf16 rows of odd length start at any element; the chunk that the row's
-// end cuts is taken element by element.
+// end cuts is taken element by element, under a branch, so each chunk waits for
+// its own loads (norm_in and its gradient, 4096 x 2559: 11.3 and 27.4 us a call;
+// 2558: 9.6 and 19.8).
 template <class A, bool STREAM>
 struct RowRef<A, true, STREAM> {
   typedef typename A::T T;
