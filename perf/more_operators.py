@@ -1,0 +1,481 @@
+"""Measured calls of the operators that train the routed experts: their gated
+feed-forward product with what its gradient needs kept (in the activation type
+or in 8 bits), that gradient, 8-bit checkpoints of activations, and the
+gradient of the router's product.
+
+Formulas (row r of expert e, pair p = sorted_pair[r], token t = p // k;
+W_gate, W_up [E][I][H], W_down [E][H][I]):
+
+  save       g = W_gate x[t], u = W_up x[t], h = silu(g) u; g and u are kept
+  checkpoint of 32 neighbours v with a = max |v|: scale 2^e, e the smallest
+             integer >= -126 with a <= 127 * 2^e, codes round(v / 2^e) (ties to
+             even), read back as code * 2^e
+  backward   dh = W_down^T dy[r], s = 1 / (1 + exp(-g)),
+             du = dh g s, dg = dh u s (1 + g (1 - s)), h = g s u
+             drows[r] = W_gate^T dg + W_up^T du
+             dW_gate = sum_r dg x[t]^T, dW_up = sum_r du x[t]^T,
+             dW_down = sum_r dy[r] h^T   (zeros for an expert without rows)
+  router     dl[p] = w_j (dw_j - sum_i w_i dw_i) of the token's k weights w
+             dx[t] = dx_in[t] + sum_j dl[t k + j] W_router[ids_j]
+             dW_router[e] = sum_(p of e) dl[p] x[p // k], dbias[e] = sum_(p of e) dl[p]
+
+``own`` selects what ``run`` computes with: elementary torch operations in
+float32, or the library's entry points.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+own = False
+
+_DEV = "cuda"
+_TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# ---------------------------------------------------------------------------
+# Cases
+# ---------------------------------------------------------------------------
+
+
+def _save(name, T, H, E, I, k, act, kept, skew=0.0):
+    return dict(name=name, kind="save", T=T, H=H, E=E, I=I, k=k, act=act, kept=kept, skew=skew,
+                drop=0.0)
+
+
+def _backward(name, T, H, E, I, k, act, kept, x8=False, skew=0.0, drop=0.0):
+    return dict(name=name, kind="backward", T=T, H=H, E=E, I=I, k=k, act=act, kept=kept, x8=x8,
+                skew=skew, drop=drop)
+
+
+def _checkpoint(name, rows, cols, act):
+    return dict(name=name, kind="checkpoint", T=rows, H=cols, act=act)
+
+
+def _router(name, T, H, E, k, act, skew=0.0, drop=0.0):
+    return dict(name=name, kind="router", T=T, H=H, E=E, k=k, act=act, skew=skew, drop=drop)
+
+
+def listed():
+    return [
+        # the tiny float32 layer: the smallest training step, bound by latency
+        _save("save_tiny", 16, 256, 16, 64, 2, "f32", "act"),
+        # one prefill window in training, g and u kept in 8 bits
+        _save("save_window", 4096, 2560, 512, 640, 10, "bf16", "8bit", skew=0.2),
+        # a gated block that every token runs through, beside the routed experts
+        _save("save_dense", 8192, 2560, 1, 5120, 1, "bf16", "act"),
+        # the gradient of the tiny float32 layer
+        _backward("backward_tiny", 16, 256, 16, 64, 2, "f32", "act"),
+        # a micro-batch of 256 tokens: five rows an expert, all weight gradients written
+        _backward("backward_micro", 256, 2560, 512, 640, 10, "bf16", "act"),
+        # one prefill window in training, everything kept in 8 bits
+        _backward("backward_window", 4096, 2560, 512, 640, 10, "bf16", "8bit", x8=True, skew=0.2),
+        # the gradient of the block that every token runs through
+        _backward("backward_dense", 8192, 2560, 1, 5120, 1, "bf16", "act"),
+        # a ragged batch, narrow experts, a tenth of the pairs dropped by a capacity
+        _backward("backward_ragged", 777, 384, 60, 96, 3, "bf16", "8bit", drop=0.1),
+        # one token row of a checkpoint, written and read back
+        _checkpoint("checkpoint_row", 1, 2560, "bf16"),
+        # eight merged prefill windows' residual stream
+        _checkpoint("checkpoint_merged", 32768, 2560, "bf16"),
+        # a ragged float32 batch
+        _router("router_ragged", 333, 384, 60, 3, "f32", drop=0.1),
+        # one prefill window in training under skewed routing
+        _router("router_window", 4096, 2560, 512, 10, "bf16", skew=0.2),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def _cost(case):
+    w = work(case)
+    return w["bytes"] / 5e12 + w["flops"] / (1e15 if case["act"] == "bf16" else 1e14)
+
+
+def draw(rng):
+    most = max(_cost(c) for c in listed())
+    kind = rng.choice(["save", "save", "backward", "backward", "backward", "checkpoint", "router"])
+    act = rng.choice(["bf16", "bf16", "f32"])
+    skew, drop = rng.choice([0.0, 0.2]), rng.choice([0.0, 0.0, 0.1])
+    T = _log_int(rng, 1, 32768 if kind == "checkpoint" else 8192)
+    if kind == "checkpoint":
+        case = _checkpoint("", T, 32 * _log_int(rng, 1, 256), act)
+    else:
+        H = rng.choice([128 * rng.randint(1, 28), 2560])
+        E = rng.choice([_log_int(rng, 1, 512), 512, 1])
+        k = rng.randint(1, min(E, 10))
+        if kind == "router":                                    # one weight alone has no gradient
+            E, k = max(E, 2), max(k, 2)
+            case = _router("", T, H, E, k, act, skew, drop)
+        else:
+            I = rng.choice([32 * rng.randint(1, 40), 640])
+            if E == 1:
+                I = 32 * _log_int(rng, 1, 160)
+            if kind == "save":
+                kept = rng.choice(["act", "8bit"]) if act == "bf16" else "act"
+                case = _save("", T, H, E, I, k, act, kept, skew)
+            else:
+                kept = rng.choice(["act", "8bit"])
+                case = _backward("", T, H, E, I, k, act, kept, kept == "8bit" and rng.random() < 0.5,
+                                 skew, drop)
+    while _cost(case) > most:
+        if case.get("E", 1) > 64:
+            case["E"] = case["E"] * 3 // 4
+        else:
+            case["T"] = max(1, case["T"] * 3 // 4)
+    del case["name"]
+    return case
+
+
+def work(case):
+    c = case
+    T, H = c["T"], c["H"]
+    a = 2 if c["act"] == "bf16" else 4
+    small = 1 + 1 / 32                                          # a code and its share of a scale
+    if c["kind"] == "checkpoint":
+        return {"bytes": round(2 * T * H * (a + small)), "flops": 4 * T * H}
+    E, k = c["E"], c["k"]
+    P = round(T * k * (1 - c["drop"]))
+    if c["kind"] == "router":
+        return {"bytes": 3 * T * H * a + E * H * (a + 4) + 12 * T * k + 4 * P + 4 * E,
+                "flops": 4 * P * H}
+    I = c["I"]
+    read = min(E, P)                                            # experts with rows, at most
+    kept = 2 * P * I * (a if c["kept"] == "act" else small)
+    if c["kind"] == "save":
+        b = T * H * a + 2 * read * I * H * a + P * I * a + kept + 4 * P
+        return {"bytes": round(b), "flops": 4 * P * I * H}
+    b = 2 * P * H * a + T * H * (small if c["x8"] else a) + kept + 4 * P
+    b += 3 * read * I * H * a + 3 * E * I * H * a
+    return {"bytes": round(b), "flops": 12 * P * I * H}
+
+
+# ---------------------------------------------------------------------------
+# Inputs
+# ---------------------------------------------------------------------------
+
+
+def _groups(v):
+    """v [..., n] as [..., n / 32, 32]."""
+    return v.reshape(*v.shape[:-1], v.shape[-1] // 32, 32)
+
+
+def _to_codes(v):
+    """(int8 codes, uint8 scales) of a matrix; a scale holds e + 127."""
+    v = _groups(v.float())
+    a = v.abs().amax(dim=-1, keepdim=True)
+    m, e = torch.frexp(a)                                       # a = m 2^e, m in [0.5, 1)
+    e = e - 7 + (m > 127 / 128).to(e.dtype)
+    e = torch.where(a > 0, e, torch.full_like(e, -126)).clamp(min=-126)
+    # v 2^-e in two exact steps: 2^-e itself may not be a float32
+    half = torch.div(-e, 2, rounding_mode="floor")
+    codes = torch.round(torch.ldexp(torch.ldexp(v, half), -e - half)).to(torch.int8)
+    return codes.flatten(-2), (e + 127).to(torch.uint8).squeeze(-1)
+
+
+def _from_codes(codes, scales):
+    """What codes and scales stand for, float32."""
+    e = scales.to(torch.int32) - 127
+    return torch.ldexp(_groups(codes.float()), e[..., None]).flatten(-2)
+
+
+def _inputs(case, seed):
+    """The case's tensors, from the seed alone."""
+    c, dt = case, _TYPES[case["act"]]
+    T, H = c["T"], c["H"]
+    g = torch.Generator(device=_DEV)
+    g.manual_seed(seed)
+
+    def normal(shape, std=1.0, dtype=dt):
+        return (torch.randn(shape, generator=g, device=_DEV) * std).to(dtype)
+
+    d = {}
+    if c["kind"] == "checkpoint":
+        # features of unlike size, as a residual stream has them
+        width = torch.exp(torch.randn(H, generator=g, device=_DEV))
+        d["v"] = (torch.randn((T, H), generator=g, device=_DEV) * width).to(dt)
+        return d
+    # routes: the k best of skewed random logits, renormalized weights; kept pairs sorted by
+    # expert, dropped ones behind them without a row
+    E, k = c["E"], c["k"]
+    P = T * k
+    logits = torch.randn((T, E), generator=g, device=_DEV)
+    if c["skew"]:
+        rank = torch.arange(1, E + 1, device=_DEV, dtype=torch.float32)
+        logits = logits - c["skew"] * torch.log(rank)
+    top, ids = torch.topk(logits, k, dim=1)
+    d["topk_ids"] = ids.to(torch.int32).contiguous()
+    d["topk_w"] = torch.softmax(top, dim=1).contiguous()
+    expert = ids.reshape(-1)
+    if c["drop"]:
+        gone = torch.rand(P, generator=g, device=_DEV) < c["drop"]
+        expert = torch.where(gone, torch.full_like(expert, E), expert)
+    order = torch.argsort(expert, stable=True)
+    counts = torch.bincount(expert, minlength=E + 1)[:E]
+    offsets = torch.zeros(E + 1, dtype=torch.int64, device=_DEV)
+    offsets[1:] = torch.cumsum(counts, dim=0)
+    n = int(offsets[E])
+    sorted_pair = torch.full((P,), -1, dtype=torch.int64, device=_DEV)
+    sorted_pair[:n] = order[:n]
+    row = torch.full((P,), -1, dtype=torch.int64, device=_DEV)
+    row[order[:n]] = torch.arange(n, device=_DEV)
+    i32 = lambda t: t.to(torch.int32).contiguous()
+    d.update(counts=i32(counts), offsets=i32(offsets), sorted_pair=i32(sorted_pair),
+             pair_row=i32(row), rows=n, most=max(int(counts.max()), 1))
+    active = torch.nonzero(counts).reshape(-1)
+    d["active"] = torch.full((E,), -1, dtype=torch.int32, device=_DEV)
+    d["active"][:len(active)] = active.to(torch.int32)
+    d["n_active"] = torch.tensor([len(active)], dtype=torch.int32, device=_DEV)
+    d["x"] = normal((T, H))
+    if c["kind"] == "router":
+        d.update(w_router=normal((E, H), 0.02), dw=normal((T, k), 1.0, torch.float32),
+                 dx_in=normal((T, H), 0.1))
+        return d
+    I = c["I"]
+    d.update(gate=normal((E, I, H), 0.02), up=normal((E, I, H), 0.02))
+    if c["kind"] == "backward":
+        std = 0.02 * math.sqrt(H)
+        d.update(down=normal((E, H, I), 0.02), dy=normal((P, H), 0.1), g=normal((P, I), std),
+                 u=normal((P, I), std), g_scale=None, u_scale=None, x_scale=None)
+        if c["kept"] == "8bit":
+            d["g"], d["g_scale"] = _to_codes(d["g"])
+            d["u"], d["u_scale"] = _to_codes(d["u"])
+        if c["x8"]:
+            d["x"], d["x_scale"] = _to_codes(d["x"])
+    return d
+
+
+def prepare(case, seed):
+    state = {"case": case, **_inputs(case, seed)}
+    if case["kind"] in ("save", "backward"):
+        _plan(state)
+    if own:
+        _own_buffers(state)
+    return state
+
+
+def _plan(s):
+    """Rows of each expert side by side, padded to the longest: their indices, which of them
+    are rows, and where each row stands."""
+    E, C, n = s["case"]["E"], s["most"], s["rows"]
+    first, count = s["offsets"][:E].long(), s["counts"].long()
+    at = torch.arange(C, device=_DEV)
+    s["there"] = at[None, :] < count[:, None]
+    s["index"] = torch.where(s["there"], first[:, None] + at, torch.zeros_like(at))
+    of = torch.repeat_interleave(torch.arange(E, device=_DEV), count)
+    s["place"] = of * C + torch.arange(n, device=_DEV) - first[of]
+    s["token"] = torch.div(s["sorted_pair"].long().clamp(min=0), s["case"]["k"],
+                           rounding_mode="floor")
+
+
+def _own_buffers(s):
+    """Descriptors, outputs and workspace that a program keeps for a shape."""
+    import sparse_moe_routed_amd as M
+    c = s["case"]
+    dt, T, H, kind = _TYPES[c["act"]], c["T"], c["H"], c["kind"]
+    new = lambda *shape, dtype=dt: torch.empty(shape, dtype=dtype, device=_DEV)
+    if kind == "checkpoint":
+        s.update(codes=new(T, H, dtype=torch.int8), scales=new(T, H // 32, dtype=torch.uint8),
+                 back=new(T, H))
+        return
+    E, k = c["E"], c["k"]
+    P = T * k
+    s["shape"] = M.make_shape(T, H, E, c.get("I", 128), k, c["act"])
+    s["perm"] = M.make_perm(s["counts"], s["offsets"], s["sorted_pair"], s["pair_row"],
+                            s["active"], s["n_active"])
+    s["ws_bytes"] = M.moe_train_workspace_size(s["shape"])
+    s["ws"] = torch.empty(max(s["ws_bytes"], 1), dtype=torch.uint8, device=_DEV)
+    if kind == "router":
+        s.update(dx=new(T, H), dw_router=new(E, H, dtype=torch.float32),
+                 dbias=new(E, dtype=torch.float32))
+        return
+    I = c["I"]
+    if kind == "save":
+        s["experts"] = M.make_experts(s["gate"], s["up"], None)
+        s["h"] = new(P, I)
+        s["g"], s["u"], s["g_scale"], s["u_scale"] = new(P, I), new(P, I), None, None
+        if c["kept"] == "8bit":
+            s["g8"], s["u8"] = new(P, I, dtype=torch.int8), new(P, I, dtype=torch.int8)
+            s["g_scale"] = new(P, I // 32, dtype=torch.uint8)
+            s["u_scale"] = new(P, I // 32, dtype=torch.uint8)
+            s["saved"] = M.make_saved(s["g8"], s["u8"], s["g_scale"], s["u_scale"])
+        else:
+            s["saved"] = M.make_saved(s["g"], s["u"])
+        return
+    s["experts"] = M.make_experts(s["gate"], s["up"], s["down"])
+    s["saved"] = M.make_saved(s["g"], s["u"], s["g_scale"], s["u_scale"])
+    s.update(drows=new(P, H), dgate=new(E, I, H), dup=new(E, I, H), ddown=new(E, H, I))
+    s["dexperts"] = M.make_experts(s["dgate"], s["dup"], s["ddown"])
+
+
+# ---------------------------------------------------------------------------
+# One pass
+# ---------------------------------------------------------------------------
+
+
+def run(state):
+    return dict(sorted((_run_own if own else _run_plain)(state).items()))
+
+
+def _run_own(s):
+    import sparse_moe_routed_amd as M
+    c, kind = s["case"], s["case"]["kind"]
+    if kind == "checkpoint":
+        M.moe_save8(c["act"], c["T"], c["H"], s["v"], s["codes"], s["scales"])
+        M.moe_restore8(c["act"], c["T"], c["H"], s["codes"], s["scales"], s["back"])
+        return {"v": s["back"]}
+    if kind == "router":
+        M.moe_router_backward(s["shape"], s["topk_ids"], s["topk_w"], s["dw"], s["x"],
+                              s["w_router"], s["perm"], s["dx_in"], s["dx"], s["dw_router"],
+                              s["dbias"], s["ws"], s["ws_bytes"])
+        return {"dx": s["dx"], "dw_router": s["dw_router"], "dbias": s["dbias"]}
+    if kind == "save":
+        P, I = c["T"] * c["k"], c["I"]
+        M.moe_ffn_gate_up_save(s["shape"], s["x"], s["experts"], s["perm"], s["saved"], s["h"],
+                               s["ws"], s["ws_bytes"])
+        if c["kept"] == "8bit":                # the values that the codes stand for
+            M.moe_restore8(c["act"], P, I, s["g8"], s["g_scale"], s["g"])
+            M.moe_restore8(c["act"], P, I, s["u8"], s["u_scale"], s["u"])
+        return {"h": s["h"], "g": s["g"], "u": s["u"]}
+    if c["drop"]:
+        s["drows"][s["rows"]:].zero_()         # rows that no pair names
+    M.moe_ffn_backward(s["shape"], s["dy"], s["x"], s["x_scale"], s["saved"], s["experts"],
+                       s["perm"], s["drows"], s["dexperts"], s["ws"], s["ws_bytes"])
+    return {"drows": s["drows"], "dgate": s["dgate"], "dup": s["dup"], "ddown": s["ddown"]}
+
+
+def _side_by_side(s, rows):
+    """[E][longest][n] float32 of the rows [P][n] (or of each row's token), zeros behind."""
+    return rows[s["index"]].float() * s["there"][:, :, None]
+
+
+def _run_plain(s):
+    c, kind = s["case"], s["case"]["kind"]
+    dt = _TYPES[c["act"]]
+    if kind == "checkpoint":
+        return {"v": _from_codes(*_to_codes(s["v"])).to(dt)}
+    T, H, E, k = c["T"], c["H"], c["E"], c["k"]
+    P = T * k
+    if kind == "router":
+        w, dw, ids = s["topk_w"], s["dw"], s["topk_ids"].long()
+        dl = w * (dw - (w * dw).sum(dim=1, keepdim=True))
+        kept = (s["pair_row"] >= 0).reshape(T, k)
+        dlogits = torch.zeros((T, E), device=_DEV).scatter_(1, ids, dl * kept)
+        dx = s["dx_in"].float() + dlogits @ s["w_router"].float()
+        return {"dx": dx.to(dt), "dw_router": dlogits.t() @ s["x"].float(),
+                "dbias": dlogits.sum(dim=0)}
+    I, n = c["I"], s["rows"]
+
+    def in_rows(v):                            # [E][longest][m] -> [P][m], zeros behind
+        out = torch.zeros((P, v.shape[2]), dtype=dt, device=_DEV)
+        out[:n] = v.reshape(-1, v.shape[2])[s["place"]].to(dt)
+        return out
+
+    x = s["x"] if c["kind"] == "save" or not c["x8"] else _from_codes(s["x"], s["x_scale"])
+    x = _side_by_side(s, x[s["token"]])
+    if kind == "save":
+        g = torch.bmm(x, s["gate"].float().transpose(1, 2).contiguous())
+        u = torch.bmm(x, s["up"].float().transpose(1, 2).contiguous())
+        h = g * torch.sigmoid(g) * u
+        if c["kept"] == "8bit":
+            g, u = _from_codes(*_to_codes(g)), _from_codes(*_to_codes(u))
+        return {"h": in_rows(h), "g": in_rows(g), "u": in_rows(u)}
+    g, u = s["g"], s["u"]
+    if c["kept"] == "8bit":
+        g, u = _from_codes(g, s["g_scale"]), _from_codes(u, s["u_scale"])
+    g, u, dy = _side_by_side(s, g), _side_by_side(s, u), _side_by_side(s, s["dy"])
+    dh = torch.bmm(dy, s["down"].float())
+    sig = torch.sigmoid(g)
+    h = g * sig * u
+    du = dh * g * sig
+    dg = dh * u * sig * (1.0 + g * (1.0 - sig))
+    drows = torch.bmm(dg, s["gate"].float()) + torch.bmm(du, s["up"].float())
+    return {"drows": in_rows(drows),
+            "dgate": torch.bmm(dg.transpose(1, 2), x).to(dt),
+            "dup": torch.bmm(du.transpose(1, 2), x).to(dt),
+            "ddown": torch.bmm(dy.transpose(1, 2), h).to(dt)}
+
+
+# ---------------------------------------------------------------------------
+# Definition in 64 bits
+# ---------------------------------------------------------------------------
+
+
+def exact(case, seed):
+    return dict(sorted(_exact(case, _inputs(case, seed)).items()))
+
+
+def _as_stored(v):
+    """A matrix in 64 bits as its 8-bit checkpoint reads back."""
+    blocks = v.reshape(v.shape[0], -1, 32)
+    peak = blocks.abs().max(dim=2).values
+    e = torch.ceil(torch.log2(peak.clamp(min=1e-300) / 127.0))
+    e = torch.where(torch.pow(2.0, e) * 127.0 < peak, e + 1, e)
+    e = torch.where(torch.pow(2.0, e - 1) * 127.0 >= peak, e - 1, e).clamp(min=-126.0)
+    step = torch.pow(2.0, e)[:, :, None]
+    return (torch.round(blocks / step) * step).reshape(v.shape)
+
+
+def _stands_for(codes, scales):
+    step = torch.pow(2.0, scales.double() - 127.0).repeat_interleave(32, dim=1)
+    return codes.double() * step
+
+
+def _exact(c, s):
+    kind = c["kind"]
+    if kind == "checkpoint":
+        return {"v": _as_stored(s["v"].double())}
+    T, H, E, k = c["T"], c["H"], c["E"], c["k"]
+    P = T * k
+    new = lambda *shape: torch.zeros(shape, dtype=torch.float64, device=_DEV)
+    ends = s["offsets"].tolist()
+    if kind == "router":
+        w, dw = s["topk_w"].double(), s["dw"].double()
+        dl = (w * dw - w * (w * dw).sum(1)[:, None]).reshape(-1)
+        dx, dwr, dbias = s["dx_in"].double(), new(E, H), new(E)
+        for e in range(E):
+            p = s["sorted_pair"][ends[e]:ends[e + 1]].long()
+            t = p // k
+            dx[t] += dl[p][:, None] * s["w_router"][e].double()[None, :]
+            dwr[e] = dl[p] @ s["x"][t].double()
+            dbias[e] = dl[p].sum()
+        return {"dx": dx, "dw_router": dwr, "dbias": dbias}
+    I = c["I"]
+    if kind == "save":
+        h, g, u = new(P, I), new(P, I), new(P, I)
+        for e in range(E):
+            a, b = ends[e], ends[e + 1]
+            if a == b:
+                continue
+            x = s["x"][s["sorted_pair"][a:b].long() // k].double()
+            g[a:b] = x @ s["gate"][e].double().t()
+            u[a:b] = x @ s["up"][e].double().t()
+            h[a:b] = g[a:b] / (1.0 + torch.exp(-g[a:b])) * u[a:b]
+        if c["kept"] == "8bit":
+            g, u = _as_stored(g), _as_stored(u)
+        return {"h": h, "g": g, "u": u}
+    drows, dgate, dup, ddown = new(P, H), new(E, I, H), new(E, I, H), new(E, H, I)
+    for e in range(E):
+        a, b = ends[e], ends[e + 1]
+        if a == b:
+            continue
+        t = s["sorted_pair"][a:b].long() // k
+        x = _stands_for(s["x"][t], s["x_scale"][t]) if c["x8"] else s["x"][t].double()
+        if c["kept"] == "8bit":
+            g = _stands_for(s["g"][a:b], s["g_scale"][a:b])
+            u = _stands_for(s["u"][a:b], s["u_scale"][a:b])
+        else:
+            g, u = s["g"][a:b].double(), s["u"][a:b].double()
+        dy = s["dy"][a:b].double()
+        dh = dy @ s["down"][e].double()
+        q = torch.exp(-g)
+        silu = g / (1.0 + q)
+        dg = dh * u * (1.0 + q + g * q) / (1.0 + q) ** 2
+        drows[a:b] = dg @ s["gate"][e].double() + (dh * silu) @ s["up"][e].double()
+        dgate[e] = dg.t() @ x
+        dup[e] = (dh * silu).t() @ x
+        ddown[e] = dy.t() @ (silu * u)
+    return {"drows": drows, "dgate": dgate, "dup": dup, "ddown": ddown}
