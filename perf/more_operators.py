@@ -79,7 +79,7 @@ def listed():
         _checkpoint("checkpoint_row", 1, 2560, "bf16"),
         # eight merged prefill windows' residual stream
         _checkpoint("checkpoint_merged", 32768, 2560, "bf16"),
-        # a ragged float32 batch
+        # a ragged float32 batch in which a capacity dropped a tenth of the pairs
         _router("router_ragged", 333, 384, 60, 3, "f32", drop=0.1),
         # one prefill window in training under skewed routing
         _router("router_window", 4096, 2560, 512, 10, "bf16", skew=0.2),
@@ -138,10 +138,10 @@ def work(case):
     if c["kind"] == "checkpoint":
         return {"bytes": round(2 * T * H * (a + small)), "flops": 4 * T * H}
     E, k = c["E"], c["k"]
-    P = round(T * k * (1 - c["drop"]))
+    P = T * k
     if c["kind"] == "router":
-        return {"bytes": 3 * T * H * a + E * H * (a + 4) + 12 * T * k + 4 * P + 4 * E,
-                "flops": 4 * P * H}
+        return {"bytes": 3 * T * H * a + E * H * (a + 4) + 16 * P + 4 * E, "flops": 4 * P * H}
+    P = round(P * (1 - c["drop"]))
     I = c["I"]
     read = min(E, P)                                            # experts with rows, at most
     kept = 2 * P * I * (a if c["kept"] == "act" else small)
@@ -210,8 +210,8 @@ def _inputs(case, seed):
     d["topk_ids"] = ids.to(torch.int32).contiguous()
     d["topk_w"] = torch.softmax(top, dim=1).contiguous()
     expert = ids.reshape(-1)
-    if c["drop"]:
-        gone = torch.rand(P, generator=g, device=_DEV) < c["drop"]
+    gone = torch.rand(P, generator=g, device=_DEV) < c["drop"]
+    if c["kind"] != "router":                  # a dropped pair's weight still shares the softmax
         expert = torch.where(gone, torch.full_like(expert, E), expert)
     order = torch.argsort(expert, stable=True)
     counts = torch.bincount(expert, minlength=E + 1)[:E]
@@ -231,8 +231,8 @@ def _inputs(case, seed):
     d["n_active"] = torch.tensor([len(active)], dtype=torch.int32, device=_DEV)
     d["x"] = normal((T, H))
     if c["kind"] == "router":
-        d.update(w_router=normal((E, H), 0.02), dw=normal((T, k), 1.0, torch.float32),
-                 dx_in=normal((T, H), 0.1))
+        dw = normal((T, k), 1.0, torch.float32).masked_fill(gone.reshape(T, k), 0.0)
+        d.update(w_router=normal((E, H), 0.02), dw=dw, dx_in=normal((T, H), 0.1))
         return d
     I = c["I"]
     d.update(gate=normal((E, I, H), 0.02), up=normal((E, I, H), 0.02))
@@ -362,8 +362,7 @@ def _run_plain(s):
     if kind == "router":
         w, dw, ids = s["topk_w"], s["dw"], s["topk_ids"].long()
         dl = w * (dw - (w * dw).sum(dim=1, keepdim=True))
-        kept = (s["pair_row"] >= 0).reshape(T, k)
-        dlogits = torch.zeros((T, E), device=_DEV).scatter_(1, ids, dl * kept)
+        dlogits = torch.zeros((T, E), device=_DEV).scatter_(1, ids, dl)
         dx = s["dx_in"].float() + dlogits @ s["w_router"].float()
         return {"dx": dx.to(dt), "dw_router": dlogits.t() @ s["x"].float(),
                 "dbias": dlogits.sum(dim=0)}
