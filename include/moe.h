@@ -549,6 +549,113 @@ int moe_combine_backward(const moe_shape* shape, const void* dout, const void* y
 int moe_route_backward(const moe_shape* shape, const int32_t* topk_ids, const float* topk_w,
                        const float* dw, float* dlogits, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Training the routed experts: the gated product with what its gradient
+ * needs kept, that gradient, 8-bit checkpoints of activations, and the
+ * gradient of the router's product.  With E = 1 and top_k = 1 the first two
+ * are a gated feed-forward block that every token runs through.
+ * ------------------------------------------------------------------------
+ * The conventions above hold.  Products and sums are accumulated in float32
+ * in an order that depends on the shape and the rows per expert only, so
+ * results repeat bit for bit; every output is rounded once, from float32,
+ * except where a call says what else it rounds.  A NaN or infinity reaches
+ * the outputs that depend on it and no others.
+ * Expert weights are dense and row-major (wfmt other than MOE_WF_DENSE is
+ * MOE_E_FORMAT, MOE_F_TILED_WEIGHTS is MOE_E_FLAGS; the scale pointers NULL);
+ * the other flags are ignored.  The two products also need (MOE_E_LIMIT
+ * otherwise): T * H * 4 < 2^32 - 256 for float32, and fewer than 2^23 tiles
+ * of 32 rows x 64 columns of h and of drows, and of 128 x 128 of the weight
+ * gradients.
+ *
+ * perm: offsets and sorted_pair are read, the rest may be NULL.  Row r of
+ * expert e (offsets[e] <= r < offsets[e+1]) belongs to pair p =
+ * sorted_pair[r] of token p / top_k.  Pairs may have been dropped after
+ * moe_permute, by giving offsets and sorted_pair of the remaining ones: rows
+ * from offsets[E] on are then neither read nor written.  Values out of range
+ * are memory-safe but give unspecified results. */
+
+/* 8-bit checkpoints.  A matrix is kept as int8 codes of its elements and one
+ * scale byte per 32 consecutive elements: the element is code * 2^(scale-127),
+ * with the smallest scale >= 1 whose 127 * 2^(scale-127) is not below the
+ * largest magnitude of the 32 (at most 248, where codes past 127 are cut to
+ * 127, so that no finite number reads back as infinity), and codes rounded to
+ * nearest even.  A power of two makes every kept value exact in bf16 and the
+ * codes independent of how the scale is applied; the rounding error is at
+ * most half a unit of the code, 1/127 of the largest magnitude.  32 elements
+ * among which is a NaN or an infinity have scale 255 and read back as NaN. */
+
+/* What the gated product keeps for its gradient: g and u [P][I], in the act
+ * type (both scale pointers NULL) or as 8-bit checkpoints (codes, and the
+ * scales [P][I/32] as uint8). */
+typedef struct {
+  void* g;
+  void* u;
+  uint8_t* g_scale;
+  uint8_t* u_scale;
+} moe_saved;
+
+/* Bytes of workspace that every call of this section needs for this shape
+ * (any valid shape; 0 for an invalid one or T == 0).  The calls keep nothing
+ * in it, so one buffer serves them all in turn, but not two calls that may
+ * run at the same time.  Host-only, pure. */
+size_t moe_train_workspace_size(const moe_shape* shape);
+
+/* Write and read an 8-bit checkpoint of a matrix of rows x cols elements
+ * (act, cols % 32 == 0, rows * cols <= 2^40, MOE_E_SHAPE / MOE_E_LIMIT
+ * otherwise): v [rows][cols] act, codes int8 [rows][cols], scales uint8
+ * [rows][cols/32].  rows == 0 is a no-op. */
+int moe_save8(int32_t act, int64_t rows, int64_t cols, const void* v, int8_t* codes,
+              uint8_t* scales, hipStream_t stream);
+int moe_restore8(int32_t act, int64_t rows, int64_t cols, const int8_t* codes,
+                 const uint8_t* scales, void* v, hipStream_t stream);
+
+/* moe_ffn_gate_up that keeps g and u: for every row r with token t
+ *   g[r][i] = sum_h W_gate[e][i][h] x[t][h],  u likewise with W_up,
+ *   h[r][i] = silu(g[r][i]) * u[r][i],
+ * all three from the float32 sums; g and u are written to `saved`.  x [T][H]
+ * act; h [P][I] act (moe_ffn_down of the same shape takes it); experts: gate
+ * and up are read, down may be NULL. */
+int moe_ffn_gate_up_save(const moe_shape* shape, const void* x, const moe_experts* experts,
+                         const moe_perm* perm, const moe_saved* saved, void* h, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+
+/* Gradient of the gated product and the down projection, for the gradient dy
+ * of y (moe_combine_backward's dy):
+ *   dh = W_down^T dy,  s = 1 / (1 + exp(-g)),
+ *   du = dh g s,  dg = dh u s (1 + g (1 - s)),  h = g s u,
+ *   drows[r] = W_gate^T dg + W_up^T du   (moe_dispatch_backward adds a token's),
+ *   dW_gate[e] = sum_r dg x[t]^T,  dW_up[e] = sum_r du x[t]^T,
+ *   dW_down[e] = sum_r dy[r] h^T   (zeros for an expert without rows).
+ * dg, du and h are rounded to the act type before the products that use
+ * them.  dy, drows [P][H] act; x [T][H] act, or with x_scale (uint8
+ * [T][H/32]) its 8-bit checkpoint; saved as moe_ffn_gate_up_save left it.
+ * drows may be NULL (not wanted), and so may dexperts, whose gate, up and
+ * down receive the weights' gradients in the act type, in the weights' layout
+ * (its scale pointers must be NULL); MOE_E_NULL without either.  x may be NULL
+ * when dexperts is.  T == 0 writes dexperts as zeros. */
+int moe_ffn_backward(const moe_shape* shape, const void* dy, const void* x,
+                     const uint8_t* x_scale, const moe_saved* saved, const moe_experts* experts,
+                     const moe_perm* perm, void* drows, const moe_experts* dexperts,
+                     void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradient of moe_route for the gradient dw of its weights:
+ *   dl[t][j] = w_j (dw_j - sum_i w_i dw_i)   (moe_route_backward's dlogits),
+ *   dx[t] = dx_in[t] + sum_j dl[t][j] w_router[topk_ids[t][j]],
+ *   dw_router[e] = sum over the pairs of expert e of dl[p] x[p / top_k],
+ *   dbias[e] = sum over the pairs of expert e of dl[p].
+ * topk_ids, topk_w, dw [T][top_k] (an id outside [0, E) adds nothing to dx);
+ * x, dx_in, dx [T][H] act; w_router [E][H] act; dw_router float [E][H]; dbias
+ * float [E].  perm is that of all pairs, as from moe_permute: the weight of a
+ * pair that was dropped later shares the softmax, so it has a gradient (its
+ * own dw is 0).  dx, dw_router and dbias may each be NULL (MOE_E_NULL if all
+ * are); dx_in may be NULL (taken as 0), w_router when dx is, x when dw_router
+ * is, perm when dw_router and dbias are.  T == 0 writes dw_router and dbias as
+ * zeros.  Any weight format and flags. */
+int moe_router_backward(const moe_shape* shape, const int32_t* topk_ids, const float* topk_w,
+                        const float* dw, const void* x, const void* w_router, const moe_perm* perm,
+                        const void* dx_in, void* dx, float* dw_router, float* dbias,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Measurement helper, not part of the layer: streams `bytes` (a non-zero
  * multiple of 16) from `buf` once with 16-byte loads spread over 2048
  * workgroups, the read-bandwidth ceiling that the layer's kernels are

@@ -16,5 +16,7 @@ from ._abi import (  # noqa: F401
     moe_combine_backward, moe_combine_norm, moe_dispatch, moe_dispatch_backward, moe_norm,
     moe_norm_in, moe_norm_in_backward, moe_norm_out, moe_norm_out_backward,
     moe_norm_workspace_size, moe_route_backward,
+    make_saved, moe_ffn_backward, moe_ffn_gate_up_save, moe_restore8, moe_router_backward,
+    moe_save8, moe_saved, moe_train_workspace_size,
 )
 from .layer import MoELayerBuffers  # noqa: F401

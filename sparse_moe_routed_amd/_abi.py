@@ -1,4 +1,5 @@
-"""Binding of libmoe.so (ctypes; the calls around the layer: _block.so):
+"""Binding of libmoe.so (ctypes; the calls around the layer and its training:
+_block.so):
 argument marshalling only.
 
 Every function has the name of the C entry point it calls.  Tensor
@@ -33,7 +34,9 @@ EXPORTS = ("moe_workspace_size", "moe_status_str", "moe_tile_experts", "moe_rout
            "moe_stream_read", "moe_layer_noalloc", "moe_route_permute",
            "moe_ffn_down_combine", "moe_norm_workspace_size", "moe_norm_in", "moe_norm_in_backward",
            "moe_norm_out", "moe_norm_out_backward", "moe_combine_norm", "moe_dispatch",
-           "moe_dispatch_backward", "moe_combine_backward", "moe_route_backward")
+           "moe_dispatch_backward", "moe_combine_backward", "moe_route_backward",
+           "moe_train_workspace_size", "moe_save8", "moe_restore8", "moe_ffn_gate_up_save",
+           "moe_ffn_backward", "moe_router_backward")
 MOE_F_TILED_WEIGHTS = 0x1
 MOE_F_CHECK_FINITE = 0x2
 MOE_F_FUSED_FFN = 0x4
@@ -67,6 +70,11 @@ class moe_perm(ctypes.Structure):
     _fields_ = [("counts", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
                 ("sorted_pair", ctypes.c_void_p), ("pair_row", ctypes.c_void_p),
                 ("active", ctypes.c_void_p), ("n_active", ctypes.c_void_p)]
+
+
+class moe_saved(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("u", ctypes.c_void_p), ("g_scale", ctypes.c_void_p),
+                ("u_scale", ctypes.c_void_p)]
 
 
 class moe_norm(ctypes.Structure):
@@ -129,6 +137,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_dispatch_backward.argtypes = [P(moe_shape)] + [vp] * 8
     lib.moe_combine_backward.argtypes = [P(moe_shape)] + [vp] * 7
     lib.moe_route_backward.argtypes = [P(moe_shape)] + [vp] * 5
+    lib.moe_train_workspace_size.argtypes = [P(moe_shape)]
+    lib.moe_train_workspace_size.restype = sz
+    lib.moe_save8.argtypes = [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64] + [vp] * 4
+    lib.moe_restore8.argtypes = lib.moe_save8.argtypes
+    lib.moe_ffn_gate_up_save.argtypes = [P(moe_shape), vp, P(moe_experts), P(moe_perm),
+                                         P(moe_saved), vp, vp, sz, vp]
+    lib.moe_ffn_backward.argtypes = [P(moe_shape), vp, vp, vp, P(moe_saved), P(moe_experts),
+                                     P(moe_perm), vp, P(moe_experts), vp, sz, vp]
+    lib.moe_router_backward.argtypes = [P(moe_shape)] + [vp] * 5 + [P(moe_perm)] + [vp] * 5 + [sz, vp]
+    for name in ("moe_save8", "moe_restore8", "moe_ffn_gate_up_save", "moe_ffn_backward",
+                 "moe_router_backward"):
+        getattr(lib, name).restype = i32
     for name in ("moe_norm_in", "moe_norm_in_backward", "moe_norm_out", "moe_norm_out_backward",
                  "moe_combine_norm", "moe_dispatch", "moe_dispatch_backward",
                  "moe_combine_backward", "moe_route_backward"):
@@ -369,7 +389,7 @@ def _load_block():
     if not os.path.exists(os.path.join(_PKG, "_block.so")):
         raise RuntimeError("_block.so is missing: build it with `python -m sparse_moe_routed_amd.build`")
     from . import _block as block
-    block.set_types(moe_shape, moe_norm)
+    block.set_types(moe_shape, moe_norm, moe_experts, moe_perm, moe_saved)
     # without a GPU the checks still answer
     _block_stream = _current_stream if torch.cuda.is_available() else lambda: 0
     _block = block
@@ -441,3 +461,41 @@ def moe_combine_backward(shape, dout, y, pair_row, topk_w, dy, dw, stream=None, 
 
 def moe_route_backward(shape, topk_ids, topk_w, dw, dlogits, stream=None, check=True) -> int:
     return _call("moe_route_backward", stream, check, shape, topk_ids, topk_w, dw, dlogits)
+
+
+# ---------------------------------------------------------------------------
+# Training the routed experts, through the same binding.
+# ---------------------------------------------------------------------------
+
+def make_saved(g, u, g_scale=None, u_scale=None) -> moe_saved:
+    return moe_saved(ptr(g), ptr(u), ptr(g_scale), ptr(u_scale))
+
+
+def moe_train_workspace_size(shape) -> int:
+    return int(load().moe_train_workspace_size(ctypes.byref(shape)))
+
+
+def moe_save8(act, rows, cols, v, codes, scales, stream=None, check=True) -> int:
+    return _call("moe_save8", stream, check, ACT.get(act, act), rows, cols, v, codes, scales)
+
+
+def moe_restore8(act, rows, cols, codes, scales, v, stream=None, check=True) -> int:
+    return _call("moe_restore8", stream, check, ACT.get(act, act), rows, cols, codes, scales, v)
+
+
+def moe_ffn_gate_up_save(shape, x, experts, perm, saved, h, workspace, workspace_bytes, stream=None,
+                         check=True) -> int:
+    return _call("moe_ffn_gate_up_save", stream, check, shape, x, experts, perm, saved, h,
+                 workspace, workspace_bytes)
+
+
+def moe_ffn_backward(shape, dy, x, x_scale, saved, experts, perm, drows, dexperts, workspace,
+                     workspace_bytes, stream=None, check=True) -> int:
+    return _call("moe_ffn_backward", stream, check, shape, dy, x, x_scale, saved, experts, perm,
+                 drows, dexperts, workspace, workspace_bytes)
+
+
+def moe_router_backward(shape, topk_ids, topk_w, dw, x, w_router, perm, dx_in, dx, dw_router,
+                        dbias, workspace, workspace_bytes, stream=None, check=True) -> int:
+    return _call("moe_router_backward", stream, check, shape, topk_ids, topk_w, dw, x, w_router,
+                 perm, dx_in, dx, dw_router, dbias, workspace, workspace_bytes)

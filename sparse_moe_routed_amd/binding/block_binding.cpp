@@ -1,5 +1,6 @@
-// Python binding of the entry points around the routed experts
-// (sparse_moe_routed_amd._block): argument checks and the call, nothing else.
+// Python binding of the entry points around the routed experts and of their
+// training (sparse_moe_routed_amd._block): argument checks and the call,
+// nothing else.
 //
 // Every function takes the descriptor structs (ctypes), the arguments of the
 // C function in its order -- each a torch tensor, an address or None -- and
@@ -20,6 +21,9 @@ namespace {
 
 PyTypeObject* g_shape_type = nullptr;   // ctypes structures of _abi.py
 PyTypeObject* g_norm_type = nullptr;
+PyTypeObject* g_experts_type = nullptr;
+PyTypeObject* g_perm_type = nullptr;
+PyTypeObject* g_saved_type = nullptr;
 
 at::ScalarType act_type(int32_t act) {
   if (act == MOE_DT_F32) return at::kFloat;
@@ -37,6 +41,17 @@ class Args {
   }
   const moe_shape* shape() { return static_cast<const moe_shape*>(structure(g_shape_type)); }
   const moe_norm* norm() { return static_cast<const moe_norm*>(structure(g_norm_type)); }
+  // None is a null pointer
+  const moe_experts* experts() { return static_cast<const moe_experts*>(optional(g_experts_type)); }
+  const moe_perm* perm() { return static_cast<const moe_perm*>(optional(g_perm_type)); }
+  const moe_saved* saved() { return static_cast<const moe_saved*>(optional(g_saved_type)); }
+
+  int64_t integer() {
+    PyObject* o = next();
+    return o ? PyLong_AsLongLong(o) : 0;
+  }
+  // whether the argument `ahead` places after the next one is given
+  bool given(Py_ssize_t ahead) const { return i_ + ahead < n_ && a_[i_ + ahead] != Py_None; }
 
   // address of a tensor of `count` elements
   void* tensor(at::ScalarType type, Count count) {
@@ -107,19 +122,26 @@ class Args {
     memory_ = MOE_E_MEMORY;
     return nullptr;
   }
+  const void* optional(PyTypeObject* type) {
+    if (!given(0)) {
+      next();
+      return nullptr;
+    }
+    return structure(type);
+  }
   const void* structure(PyTypeObject* type) {
     static const char zeros[64] = {};   // read in place of a struct that is not there
     PyObject* o = next();
     if (!o) return zeros;
     if (!type || !PyObject_TypeCheck(o, type) || PyObject_GetBuffer(o, &view_[views_], PyBUF_SIMPLE)) {
-      if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "expected a moe_shape / moe_norm");
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "expected another descriptor");
       return zeros;
     }
     return view_[views_++].buf;
   }
   PyObject* const* a_;
   Py_ssize_t n_, i_ = 0;
-  Py_buffer view_[2];
+  Py_buffer view_[5];   // moe_ffn_backward has the most
   int views_ = 0;
   int status_ = 0, memory_ = 0, device_ = -1;
 };
@@ -274,16 +296,104 @@ PyObject* route_backward(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   return a.call([&] { return moe_route_backward(s, ids, w, dw, dlogits, st); });
 }
 
-// The ctypes classes of moe_shape and moe_norm, once at import.
+PyObject* save8(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+  Args a(argv, argc);
+  const int32_t act = static_cast<int32_t>(a.integer());
+  const int64_t rows = a.integer(), cols = a.integer();
+  const Count n = static_cast<Count>(rows) * cols;
+  void* v = a.tensor(act_type(act), n);
+  int8_t* codes = static_cast<int8_t*>(a.tensor(at::kChar, n));
+  uint8_t* scales = static_cast<uint8_t*>(a.tensor(at::kByte, n / 32));
+  hipStream_t st = a.stream();
+  return a.call([&] { return moe_save8(act, rows, cols, v, codes, scales, st); });
+}
+
+PyObject* restore8(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+  Args a(argv, argc);
+  const int32_t act = static_cast<int32_t>(a.integer());
+  const int64_t rows = a.integer(), cols = a.integer();
+  const Count n = static_cast<Count>(rows) * cols;
+  const int8_t* codes = static_cast<int8_t*>(a.tensor(at::kChar, n));
+  const uint8_t* scales = static_cast<uint8_t*>(a.tensor(at::kByte, n / 32));
+  void* v = a.tensor(act_type(act), n);
+  hipStream_t st = a.stream();
+  return a.call([&] { return moe_restore8(act, rows, cols, codes, scales, v, st); });
+}
+
+PyObject* ffn_gate_up_save(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+  Args a(argv, argc);
+  const moe_shape* s = a.shape();
+  const at::ScalarType t = act_type(s->act);
+  void* x = a.tensor(t, tokens(s));
+  const moe_experts* ex = a.experts();
+  const moe_perm* pm = a.perm();
+  const moe_saved* sv = a.saved();
+  void* h = a.tensor(t, pairs(s) * s->I);
+  size_t bytes;
+  void* ws = a.workspace(&bytes);
+  hipStream_t st = a.stream();
+  return a.call([&] { return moe_ffn_gate_up_save(s, x, ex, pm, sv, h, ws, bytes, st); });
+}
+
+PyObject* ffn_backward(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+  Args a(argv, argc);
+  const moe_shape* s = a.shape();
+  const at::ScalarType t = act_type(s->act);
+  void* dy = a.tensor(t, pairs(s) * s->H);
+  void* x = a.tensor(a.given(1) ? at::kChar : t, tokens(s));
+  const uint8_t* x_scale = static_cast<uint8_t*>(a.tensor(at::kByte, tokens(s) / 32));
+  const moe_saved* sv = a.saved();
+  const moe_experts* ex = a.experts();
+  const moe_perm* pm = a.perm();
+  void* drows = a.tensor(t, pairs(s) * s->H);
+  const moe_experts* dex = a.experts();
+  size_t bytes;
+  void* ws = a.workspace(&bytes);
+  hipStream_t st = a.stream();
+  return a.call([&] {
+    return moe_ffn_backward(s, dy, x, x_scale, sv, ex, pm, drows, dex, ws, bytes, st);
+  });
+}
+
+PyObject* router_backward(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+  Args a(argv, argc);
+  const moe_shape* s = a.shape();
+  const at::ScalarType t = act_type(s->act);
+  const Count P = pairs(s), m = tokens(s), w = static_cast<Count>(s->E) * s->H;
+  const int32_t* ids = static_cast<int32_t*>(a.tensor(at::kInt, P));
+  const float* topk_w = static_cast<float*>(a.tensor(at::kFloat, P));
+  const float* dw = static_cast<float*>(a.tensor(at::kFloat, P));
+  void* x = a.tensor(t, m);
+  void* w_router = a.tensor(t, w);
+  const moe_perm* pm = a.perm();
+  void* dx_in = a.tensor(t, m);
+  void* dx = a.tensor(t, m);
+  float* dw_router = static_cast<float*>(a.tensor(at::kFloat, w));
+  float* dbias = static_cast<float*>(a.tensor(at::kFloat, s->E));
+  size_t bytes;
+  void* ws = a.workspace(&bytes);
+  hipStream_t st = a.stream();
+  return a.call([&] {
+    return moe_router_backward(s, ids, topk_w, dw, x, w_router, pm, dx_in, dx, dw_router, dbias, ws,
+                               bytes, st);
+  });
+}
+
+// The ctypes classes of the descriptors, once at import.
 PyObject* set_types(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
-  if (argc != 2 || !PyType_Check(argv[0]) || !PyType_Check(argv[1])) {
-    PyErr_SetString(PyExc_TypeError, "expected the moe_shape and moe_norm classes");
+  PyTypeObject** const types[] = {&g_shape_type, &g_norm_type, &g_experts_type, &g_perm_type,
+                                  &g_saved_type};
+  constexpr Py_ssize_t n = sizeof(types) / sizeof(types[0]);
+  bool ok = argc == n;
+  for (Py_ssize_t i = 0; ok && i < n; ++i) ok = PyType_Check(argv[i]);
+  if (!ok) {
+    PyErr_SetString(PyExc_TypeError, "expected the classes moe_shape, moe_norm, moe_experts, moe_perm, moe_saved");
     return nullptr;
   }
-  Py_INCREF(argv[0]);
-  Py_INCREF(argv[1]);
-  g_shape_type = reinterpret_cast<PyTypeObject*>(argv[0]);
-  g_norm_type = reinterpret_cast<PyTypeObject*>(argv[1]);
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    Py_INCREF(argv[i]);
+    *types[i] = reinterpret_cast<PyTypeObject*>(argv[i]);
+  }
   Py_RETURN_NONE;
 }
 
@@ -300,6 +410,11 @@ PyMethodDef g_methods[] = {
     {"moe_dispatch_backward", fast(dispatch_backward), METH_FASTCALL, nullptr},
     {"moe_combine_backward", fast(combine_backward), METH_FASTCALL, nullptr},
     {"moe_route_backward", fast(route_backward), METH_FASTCALL, nullptr},
+    {"moe_save8", fast(save8), METH_FASTCALL, nullptr},
+    {"moe_restore8", fast(restore8), METH_FASTCALL, nullptr},
+    {"moe_ffn_gate_up_save", fast(ffn_gate_up_save), METH_FASTCALL, nullptr},
+    {"moe_ffn_backward", fast(ffn_backward), METH_FASTCALL, nullptr},
+    {"moe_router_backward", fast(router_backward), METH_FASTCALL, nullptr},
     {"set_types", fast(set_types), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -191,4 +191,44 @@ hipError_t launch_route_bwd(const moe_shape& s, const int32_t* ids, const float*
 hipError_t launch_combine(const moe_shape& s, const void* y, const int32_t* pair_row,
                           const float* w, const void* residual, void* out, hipStream_t st);
 
+// Training the routed experts (k_train.hip, k_save8.hip, k_router_bwd.hip).
+// Workspace of one shape; the regions of the two products and of the router's
+// gradient overlap, as no call uses both.
+struct TrainPlan {
+  int bm;               // rows of a tile of the row products
+  int max_tiles;        // upper bound on tiles
+  size_t tiles_off;     // int32 [3 * max_tiles] (expert, row0, rows), then n_tiles
+  size_t token_off;     // int32 [P], token of each row
+  size_t x_off;         // act [T][H], x read back from an 8-bit checkpoint
+  size_t dg_off, du_off, h_off;   // act [P][I]
+  size_t dl_off;        // router: float [P]
+  size_t part_off;      // router: float [splits][E][H + 1] partial sums (splits > 1)
+  int splits;           // router: parts of an expert's rows
+  size_t total;
+};
+void make_train_plan(const moe_shape& s, TrainPlan* p);
+bool train_fits(const moe_shape& s, const TrainPlan& p);   // the limits of the two products
+
+hipError_t launch_save8(bool f32, size_t n, const void* v, int8_t* codes, uint8_t* scales,
+                        hipStream_t st);
+hipError_t launch_restore8(bool f32, size_t n, const int8_t* codes, const uint8_t* scales, void* v,
+                           hipStream_t st);
+hipError_t launch_gate_up_save(const moe_shape& s, const TrainPlan& pl, const void* x,
+                               const moe_experts& ex, const moe_perm& pm, const moe_saved& sv,
+                               void* h, void* ws, hipStream_t st);
+hipError_t launch_ffn_backward(const moe_shape& s, const TrainPlan& pl, const void* dy,
+                               const void* x, const uint8_t* x_scale, const moe_saved* sv,
+                               const moe_experts& ex, const moe_perm* pm, void* drows,
+                               const moe_experts* dex, void* ws, hipStream_t st);
+struct RouterBwd {
+  const int32_t* ids;
+  const float *w, *dw;
+  const void *x, *w_router, *dx_in;
+  const int32_t *offsets, *sorted_pair;
+  void* dx;
+  float *dw_router, *dbias, *dl, *part;
+};
+hipError_t launch_router_bwd(const moe_shape& s, const TrainPlan& pl, const RouterBwd& a,
+                             hipStream_t st);
+
 }  // namespace moe

@@ -155,6 +155,84 @@ class MoELayerBuffers:
         """moe_route_backward of this buffer's topk_ids and topk_w."""
         return _abi.moe_route_backward(self.shape, self.topk_ids, self.topk_w, dw, dlogits, stream)
 
+    def _train(self, kept=None):
+        """Memory for training, once: the workspace, gradients of the rows and
+        route weights, and g and u ('act', or '8bit' with their scales)."""
+        dev, dt, P = self.topk_ids.device, self.y.dtype, self.T * self.k
+        if not hasattr(self, "train_ws"):
+            self.train_ws_bytes = _abi.moe_train_workspace_size(self.shape)
+            self.train_ws = torch.empty(max(self.train_ws_bytes, 1), dtype=torch.uint8, device=dev)
+        if kept is not None and kept != getattr(self, "kept", None):
+            if kept not in ("act", "8bit"):
+                raise ValueError(f"kept must be 'act' or '8bit', not {kept!r}")
+            self.g_scale = self.u_scale = None
+            if kept == "8bit":
+                dt = torch.int8
+                self.g_scale = torch.empty((P, self.I // 32), dtype=torch.uint8, device=dev)
+                self.u_scale = torch.empty((P, self.I // 32), dtype=torch.uint8, device=dev)
+            self.g = torch.empty((P, self.I), dtype=dt, device=dev)
+            self.u = torch.empty((P, self.I), dtype=dt, device=dev)
+            self.saved = _abi.make_saved(self.g, self.u, self.g_scale, self.u_scale)
+            self.kept = kept
+
+    def ffn_gate_up_save(self, x, experts, kept="act", perm=None, h=None, stream=None):
+        """moe_ffn_gate_up_save into this buffer's h and saved (g and u, kept in
+        the activation type or in 8 bits)."""
+        self._train(kept)
+        return _abi.moe_ffn_gate_up_save(self.shape, x, experts, self.perm if perm is None else perm,
+                                         self.saved, self.h if h is None else h, self.train_ws,
+                                         self.train_ws_bytes, stream)
+
+    def ffn_backward(self, dy, x, experts, drows=None, dexperts=None, x_scale=None, perm=None,
+                     stream=None):
+        """moe_ffn_backward from this buffer's saved."""
+        self._train()
+        return _abi.moe_ffn_backward(self.shape, dy, x, x_scale, self.saved, experts,
+                                     self.perm if perm is None else perm, drows, dexperts,
+                                     self.train_ws, self.train_ws_bytes, stream)
+
+    def router_backward(self, dw, x, w_router, dx=None, dw_router=None, dbias=None, dx_in=None,
+                        stream=None):
+        """moe_router_backward of this buffer's topk_ids, topk_w and perm."""
+        self._train()
+        return _abi.moe_router_backward(self.shape, self.topk_ids, self.topk_w, dw, x, w_router,
+                                        self.perm, dx_in, dx, dw_router, dbias, self.train_ws,
+                                        self.train_ws_bytes, stream)
+
+    def layer_save(self, x, w_router, bias, experts, residual=None, out=None, kept="act", stream=None):
+        """The whole layer, keeping in this buffer what layer_backward needs (the
+        routes, the permutation, y, g and u).  experts are dense and row-major.
+        A buffer with check_finite is refused (MOE_E_FLAGS): these steps do not
+        check."""
+        if self.shape.flags & _abi.MOE_F_CHECK_FINITE:
+            raise _abi.MoEError(10, "MoELayerBuffers.layer_save with check_finite")
+        self.route_permute(x, w_router, bias, logits=False, stream=stream)
+        self.ffn_gate_up_save(x, experts, kept, stream=stream)
+        self.ffn_down(experts, stream=stream)
+        return self.combine(residual, out=out, stream=stream)
+
+    def layer_backward(self, dout, x, w_router, experts, dx, dw_router=None, dbias=None,
+                       dexperts=None, dx_in=None, x_scale=None, stream=None):
+        """Gradient of layer_save for the gradient dout of its output: dx [T][H]
+        (plus dx_in, for instance dout where the residual was x), dw_router,
+        dbias and dexperts (a moe_experts of the weights' gradients), each of
+        the last three only if given.  x may be its 8-bit checkpoint
+        (x_scale)."""
+        self._train()
+        if not hasattr(self, "dy"):
+            self.dy, self.drows = torch.empty_like(self.y), torch.empty_like(self.y)
+            self.dw, self.dx_rows = torch.empty_like(self.topk_w), torch.empty_like(self.out)
+        if x_scale is not None:
+            if not hasattr(self, "x_back"):
+                self.x_back = torch.empty_like(self.out)
+            _abi.moe_restore8(self.act, self.T, self.H, x, x_scale, self.x_back, stream)
+            x = self.x_back
+        self.combine_backward(dout, self.dy, self.dw, stream=stream)
+        self.ffn_backward(self.dy, x, experts, self.drows, dexperts, stream=stream)
+        self.dispatch_backward(self.drows, self.dx_rows, dx_in, stream=stream)
+        return self.router_backward(self.dw, x, w_router, dx, dw_router, dbias, self.dx_rows,
+                                    stream=stream)
+
     def layer(self, x, w_router, bias, experts, residual=None, out=None, use_perm=True,
               stream=None):
         return _abi.moe_layer(self.shape, x, w_router, bias, experts, residual,
