@@ -1,13 +1,15 @@
 // Device helpers of the training kernels: tiles of two matrices staged through
 // LDS and multiplied on the matrix cores, for bf16 and float32 alike.
 //
-// A product D[m][n] = sum_k M(m, k) N(n, k) is computed in tiles of BM x 128
-// outputs by four waves, 2 x 2, each BM/2 x 64.  A stage holds 128 bytes of k
-// per row: 64 bf16 or 32 float32.  The N side is MFMA's first operand and the
-// M side its second, so a lane of the result (i = lane % 16, q = lane / 16)
-// holds values of column-index q and row-index i: with n = 16 q + 4 f + j for
-// fragment f it owns 16 neighbouring n of one row m, which it stores itself in
-// 16-byte pieces.
+// A product D[m][n] = sum_k M(m, k) N(n, k) is computed in tiles, each wave 64
+// columns (n) of 64 or 16 rows (m).  Many rows: 128 x 256 outputs by eight waves
+// (2 x 4), three stages in LDS (144 KB, one workgroup per CU).  Few rows: 32 x
+// 128 by four waves (2 x 2), two stages (40 KB, four workgroups).  A stage holds
+// 128 bytes of k per row: 64 bf16 or 32 float32.  The N side is MFMA's first
+// operand and the M side its second, so a lane of the result (i = lane % 16, q =
+// lane / 16) holds columns 4 q .. 4 q + 3 of a fragment's 16 and row i: after one
+// exchange between lanes it stores 8 neighbouring columns (16 bytes of bf16)
+// of its row itself.
 //
 // Either side comes in one of two forms:
 //   rows:    k is contiguous in memory.  LDS holds [row][128 bytes of k].
@@ -29,9 +31,9 @@ namespace moe {
 #define MOE_LDS __attribute__((address_space(3)))
 
 constexpr int kStageBytes = 128;            // bytes of k per row and stage
-constexpr int kSideBytes = 128 * kStageBytes;
+constexpr int kBlockBytes = 128 * kStageBytes;   // 128 rows, or 128 columns, of a stage
 constexpr uint32_t kBufBytes = 0xFFFFFF00u; // no valid offset reaches it
-constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // past every buffer: zeros
+constexpr uint32_t kNowhere = kBufBytes;    // past every buffer: reads zeros, writes nothing
 
 struct TBf16 {
   typedef uint16_t T;
@@ -61,15 +63,28 @@ struct TF32 {
   static __device__ __forceinline__ float exp_neg(float g) { return expf(-g); }
 };
 
-typedef __amdgpu_buffer_rsrc_t Rsrc;
-
-__device__ __forceinline__ Rsrc buffer(const void* p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(kBufBytes),
-                                           0x00020000);
+// A raw buffer as its four words (uniform), for the loads below.
+__device__ __forceinline__ u32x4_t buffer(const void* p) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return u32x4_t{static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32) & 0xffffu, kBufBytes, 0x00020000u};
 }
 
-__device__ __forceinline__ void load_lds(Rsrc rs, char* lds, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (MOE_LDS void*)lds, 16, static_cast<int>(off), 0, 0, 0);
+// 64 lanes x 16 (or 4) bytes from the buffer to LDS, lane l's at lds + 16 l (4 l).
+// Written as assembly because the compiler, which knows that such a load
+// writes LDS but not where, waits for all of them before the next transposing
+// LDS read; here the waits are stage_barrier()'s.  Nothing but LDS is written,
+// and the registers are read when the load is issued.  The five wait states in
+// front are what a buffer load needs after the vector unit has written one
+// of its scalar registers.
+__device__ __forceinline__ void load_lds(u32x4_t rs, char* lds, uint32_t off) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS char*)lds)));
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               ::"v"(off), "s"(rs), "s"(at) : "memory");
+}
+__device__ __forceinline__ void load_lds_word(u32x4_t rs, char* lds, uint32_t off) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS char*)lds)));
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               ::"v"(off), "s"(rs), "s"(at) : "memory");
 }
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
@@ -79,25 +94,20 @@ __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane
 __device__ __forceinline__ int key_rows_m(int row) { return (row >> 1) & 7; }
 // Rows form, N side (gate and up): rows 8 (i / 4) + i % 4 are read together.
 __device__ __forceinline__ int key_rows_n(int row) { return ((row >> 1) & 1) | (((row >> 3) & 3) << 1); }
-// Columns form: per k row, bf16 (k rows 8 q + 0..3 together) and float32 (4 q).
+// Columns form, per k row: bf16 reads k rows 8 q + 0..3 together, float32 4 q.
 template <class E>
-__device__ __forceinline__ int key_cols_n(int k) {
-  if constexpr (E::SZ == 2) return (k & 3) | (((k >> 3) & 1) << 3);
-  return (k >> 2) & 3;
-}
-template <class E>
-__device__ __forceinline__ int key_cols_m(int k) {
+__device__ __forceinline__ int key_cols(int k) {
   if constexpr (E::SZ == 2) return ((k & 3) << 1) | (((k >> 3) & 1) << 3);
   return ((k >> 2) & 3) << 2;
 }
 
-// Load j of wave w covers 1 KB of a side: 8 rows of the rows form (lane l: row
-// 8 (4 j + w) + l / 8, position l % 8), or 1024 / (128 SZ) k rows of the
-// columns form.
-__device__ __forceinline__ int rows_row(int j, int w, int l) { return 8 * (4 * j + w) + (l >> 3); }
+// Load number i covers 1 KB of a side.  Rows form: rows 8 i .. 8 i + 7 (lane l: row
+// 8 i + l / 8, position l % 8).  Columns form, in blocks of 128 columns (16
+// loads): 1024 / (128 SZ) k rows of block i / 16.
+__device__ __forceinline__ int rows_row(int i, int l) { return 8 * i + (l >> 3); }
 template <class E>
-__device__ __forceinline__ int cols_k(int j, int w, int l) {
-  return E::SZ == 2 ? 4 * (4 * j + w) + (l >> 4) : 2 * (4 * j + w) + (l >> 5);
+__device__ __forceinline__ int cols_k(int i, int l) {
+  return E::SZ == 2 ? 4 * (i & 15) + (l >> 4) : 2 * (i & 15) + (l >> 5);
 }
 template <class E>
 __device__ __forceinline__ int cols_pos(int l) { return l & (E::SZ * 8 - 1); }
@@ -109,10 +119,12 @@ __device__ __forceinline__ u32x4_t frag_rows_m(const char* s, int m0, int t, int
   const int i = lane & 15, q = lane >> 4, row = m0 + 16 * t + i;
   return ld16(s + row * kStageBytes + (((q + 4 * ks) ^ key_rows_m(row)) << 4));
 }
-// rows form, N side: fragment f of wave wn: gate (f < 2) or up rows 32 wn + 8 (i / 4) + 4 (f % 2) + i % 4
+// rows form, N side: fragment f of wave wn of NW: row 32 wn + 8 (i / 4) + 4 (f % 2) + i % 4 of
+// gate (f < 2) or of up, behind the 32 NW rows of gate
+template <int NW>
 __device__ __forceinline__ u32x4_t frag_rows_n(const char* s, int wn, int f, int ks, int lane) {
   const int i = lane & 15, q = lane >> 4;
-  const int row = 64 * (f >> 1) + 32 * wn + 8 * (i >> 2) + 4 * (f & 1) + (i & 3);
+  const int row = 32 * NW * (f >> 1) + 32 * wn + 8 * (i >> 2) + 4 * (f & 1) + (i & 3);
   return ld16(s + row * kStageBytes + (((q + 4 * ks) ^ key_rows_n(row)) << 4));
 }
 
@@ -122,45 +134,21 @@ __device__ __forceinline__ u32x2_t lds_transposed(const char* p) {
   return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS v4s*)p));
 }
 
-// columns form: the fragment's column of result lane i lies in 8-byte chunk
-// i / 4 of four (4 bf16 each), element i % 4.  The transposing read takes, in
-// each group of 16 lanes, lane 4 r + c's 8 bytes as chunk c of k row r and
-// hands lane i the four k of its column.
-// N side: column 64 wn + 16 (i / 4) + 4 (f ^ ((i / 4) % 2)) + i % 4: odd lane groups
-// take their fragments in swapped order, so that one read meets both halves
-// of the 16-byte chunks (unswap() puts the results back).
+// columns form: fragment f holds columns 64 half + 16 f + i of a block.  The
+// transposing read takes, in each group of 16 lanes, lane 4 r + c's 8 bytes as
+// columns 4 c .. 4 c + 3 of k row r and hands lane i the four k of column i.
 template <class E>
-__device__ __forceinline__ u32x4_t frag_cols_n(const char* s, int wn, int f, int ks, int lane) {
+__device__ __forceinline__ u32x4_t frag_cols(const char* s, int half, int f, int ks, int lane) {
   const int s16 = lane & 15, q = lane >> 4;
   if constexpr (E::SZ == 2) {
     const int c = s16 & 3, k = 32 * ks + 8 * q + (s16 >> 2);
-    const int byte = 128 * wn + 32 * c + 8 * (f ^ (c & 1));
-    const char* p = s + k * 256 + (((byte >> 4) ^ key_cols_n<E>(k)) << 4) + (byte & 8);
+    const int byte = 128 * half + 32 * f + 8 * c;
+    const char* p = s + k * 256 + (((byte >> 4) ^ key_cols<E>(k)) << 4) + (byte & 8);
     const u32x2_t lo = lds_transposed(p), hi = lds_transposed(p + 4 * 256);
     return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
   } else {
-    const int c = s16 >> 2, k = 16 * ks + 4 * q;
-    const int chunk = 16 * wn + 4 * c + (f ^ (c & 1));
-    const char* p = s + k * 512 + ((chunk ^ key_cols_n<E>(k)) << 4) + 4 * (s16 & 3);
-    u32x4_t v;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(p + j * 512);
-    return v;
-  }
-}
-// M side: column 64 wm + 16 t + i
-template <class E>
-__device__ __forceinline__ u32x4_t frag_cols_m(const char* s, int wm, int t, int ks, int lane) {
-  const int s16 = lane & 15, q = lane >> 4;
-  if constexpr (E::SZ == 2) {
-    const int c = s16 & 3, k = 32 * ks + 8 * q + (s16 >> 2);
-    const int byte = 128 * wm + 32 * t + 8 * c;
-    const char* p = s + k * 256 + (((byte >> 4) ^ key_cols_m<E>(k)) << 4) + (byte & 8);
-    const u32x2_t lo = lds_transposed(p), hi = lds_transposed(p + 4 * 256);
-    return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-  } else {
-    const int k = 16 * ks + 4 * q, chunk = 16 * wm + 4 * t + (s16 >> 2);
-    const char* p = s + k * 512 + ((chunk ^ key_cols_m<E>(k)) << 4) + 4 * (s16 & 3);
+    const int k = 16 * ks + 4 * q, chunk = 16 * half + 4 * f + (s16 >> 2);
+    const char* p = s + k * 512 + ((chunk ^ key_cols<E>(k)) << 4) + 4 * (s16 & 3);
     u32x4_t v;
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(p + j * 512);
@@ -168,33 +156,84 @@ __device__ __forceinline__ u32x4_t frag_cols_m(const char* s, int wm, int t, int
   }
 }
 
-// Results of frag_cols_n in the order of n: v[4 f + j] of lane group q is column 16 q + 4 f + j.
-__device__ __forceinline__ void unswap(f32x4_t (&a)[4], int lane, float (&v)[16]) {
-  const bool odd = (lane >> 4) & 1;
+// A lane's results of a row: fragment f holds columns 16 f + 4 q .. + 3.  Exchanging
+// fragments f and f + 1 between lane groups q and q ^ 1 leaves each lane with 8
+// neighbouring columns, pair_col(f / 2) .. + 7, of the 32.
+__device__ __forceinline__ void swap_pair(float& a, float& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ int pair_col(int pair, int lane) {
+  const int q = lane >> 4;
+  return 32 * pair + 16 * (q & 1) + 8 * (q >> 1);
+}
+// the 8 columns of fragments 2 pair and 2 pair + 1
+__device__ __forceinline__ void pair_vals(const f32x4_t (&a)[4], int pair, float (&v)[8]) {
 #pragma unroll
-  for (int f = 0; f < 4; ++f)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[4 * f + j] = odd ? a[f ^ 1][j] : a[f][j];
+  for (int j = 0; j < 4; ++j) {
+    v[j] = a[2 * pair][j];
+    v[4 + j] = a[2 * pair + 1][j];
+    swap_pair(v[j], v[4 + j]);
+  }
 }
 
-// Two-buffered main loop: stage s + 1 is in flight while stage s is multiplied.
-// One barrier a stage: it waits for the own loads (and so, behind it, all
-// waves' loads have landed) and says that the other buffer is free again.
-template <class Issue, class Compute>
-__device__ __forceinline__ void stage_loop(int stages, char* n0, char* m0, char* n1, char* m1,
-                                           Issue&& issue, Compute&& compute) {
+// This wave's loads into LDS but for the `YOUNGER` memory operations issued
+// after them are done, and so, behind the barrier, are those of all waves; all
+// LDS reads before it are done too.  Memory operations count in order of issue.
+template <int YOUNGER>
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(YOUNGER) : "memory");
+}
+
+// Keeps instructions on either side apart.
+__device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// What one MFMA step reads from LDS.
+template <int MF>
+struct Frags {
+  u32x4_t n[4], m[MF];
+};
+
+// Main loop over a ring of R stages in LDS, GROUP loads a wave and stage.  The
+// fragments of a step are read while the step before it is multiplied, so LDS
+// and the matrix cores work at the same time (reads and products in turn, by
+// all waves together behind each barrier, took 1.4 times as long).  The barrier
+// of stage s stands between its two steps: behind it the loads of stage s + 1
+// have landed and all of stage s has been read, so stage s + R goes into its
+// place at once.
+//   issue(s, stage): starts the loads of stage s;  read(stage, ks, frags);  mma(frags)
+template <int R, int GROUP, class F, class Issue, class Read, class Mma>
+__device__ __forceinline__ void ring_loop(int stages, char* ring, int bytes, F& even, F& odd, Issue&& issue,
+                                          Read&& read, Mma&& mma) {
   if (stages <= 0) return;
-  issue(0, n0, m0);
-  for (int s = 0;;) {
-    __syncthreads();
-    if (s + 1 < stages) issue(s + 1, n1, m1);
-    compute(n0, m0);
-    if (++s >= stages) break;
-    __syncthreads();
-    if (s + 1 < stages) issue(s + 1, n0, m0);
-    compute(n1, m1);
-    if (++s >= stages) break;
+#pragma unroll
+  for (int s = 0; s < R; ++s)
+    if (s < stages) issue(s, ring + s * bytes);
+  if (stages >= R)
+    stage_barrier<GROUP * (R - 1)>();
+  else
+    stage_barrier<0>();
+  read(ring, 0, even);
+  int now = 0;   // offset of stage s
+  for (int s = 0;; ++s) {
+    read(ring + now, 1, odd);
+    sched_fence();
+    mma(even);
+    if (s + 1 == stages) break;
+    const int next = now == (R - 1) * bytes ? 0 : now + bytes;
+    sched_fence();
+    if (s + R - 1 < stages)
+      stage_barrier<GROUP * (R - 2)>();
+    else
+      stage_barrier<0>();
+    if (s + R < stages) issue(s + R, ring + now);
+    read(ring + next, 0, even);
+    sched_fence();
+    mma(odd);
+    now = next;
   }
+  mma(odd);
 }
 
 // 16-byte pieces of N elements to and from memory
@@ -207,6 +246,20 @@ __device__ __forceinline__ void store_vals(typename E::T* p, const float (&v)[N]
 #pragma unroll
     for (int e = 0; e < V; ++e) t[e] = v[c * V + e];
     *reinterpret_cast<u32x4_t*>(p + c * V) = E::Row::pack(t);
+  }
+}
+// ... to an offset of a buffer: the same number of stores whatever `off` is
+template <class E, int N>
+__device__ __forceinline__ void store_vals(const void* base, uint32_t off, const float (&v)[N]) {
+  constexpr int V = E::Row::VEC;
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<void*>(base), 0, static_cast<int>(kBufBytes), 0x00020000);
+#pragma unroll
+  for (int c = 0; c < N / V; ++c) {
+    float t[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) t[e] = v[c * V + e];
+    __builtin_amdgcn_raw_buffer_store_b128(E::Row::pack(t), rs, static_cast<int>(off + 16 * c), 0, 0);
   }
 }
 template <class E, int N>

@@ -232,6 +232,26 @@ def test_all_rows_on_one_expert(act):
     assert all(bool((o.t[:17] == 0).all()) and bool((o.t[18:] == 0).all()) for o in c.dw)
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("H,I", [(2560, 32), (1152, 160)])
+def test_strips_of_many_experts(H, I, act):
+    """Enough tiles of weight gradients that a workgroup takes several side by
+    side: experts without rows, with one stage of rows, two, and many."""
+    T, E = 1500, 1024
+    g = torch.Generator().manual_seed(13)
+    experts = torch.randint(0, E, (T, 1), generator=g)
+    for e, n in ((3, 300), (5, 100), (1023, 70), (700, 64), (701, 65), (702, 128), (703, 129)):
+        experts[torch.randperm(T, generator=g)[:n]] = e
+    c = Case(T, H, E, I, 1, act, experts=experts, seed=13)
+    c.fill_saved()
+    c.backward()
+    c.check_backward(f"strips {H} {I} {act}")
+    first = {n: v.clone() for n, v in c.grads().items()}
+    for _ in range(3):
+        c.backward()
+        assert all(torch.equal(v, first[n]) for n, v in c.grads().items())
+
+
 @pytest.mark.parametrize("kept", ["act", "8bit"])
 @pytest.mark.parametrize("T,E,k", [(50, 9, 2), (260, 2, 2)])
 def test_small_integers_are_exact(T, E, k, kept):
