@@ -191,16 +191,26 @@ hipError_t launch_route_bwd(const moe_shape& s, const int32_t* ids, const float*
 hipError_t launch_combine(const moe_shape& s, const void* y, const int32_t* pair_row,
                           const float* w, const void* residual, void* out, hipStream_t st);
 
-// Training the routed experts (k_train.hip, k_save8.hip, k_router_bwd.hip).
+// Training the routed experts (k_train*.hip, k_save8.hip, k_router_bwd.hip).
+// How one product over the experts' rows is cut: the tile shape, and into how
+// many parts its sum (float32 partial results, joined by another launch).
+enum RowShape { kRowsFew = 0, kRowsMany = 1, kRowsWide = 2 };
+struct RowCut {
+  int shape;   // RowShape
+  int parts;
+};
+constexpr int row_height(int shape) { return shape == kRowsFew ? 32 : shape == kRowsMany ? 128 : 256; }
+constexpr int kLookupExperts = 64;   // up to here a wave finds its tile itself
 // Workspace of one shape; the regions of the two products and of the router's
 // gradient overlap, as no call uses both.
 struct TrainPlan {
-  int bm;               // rows of a tile of the row products
-  int max_tiles;        // upper bound on tiles
-  size_t tiles_off;     // int32 [3 * max_tiles] (expert, row0, rows), then n_tiles
-  size_t token_off;     // int32 [P], token of each row
+  RowCut gate_up, dh, dx;
+  // tile lists, by row height 32 or 128 / 256: int32 [3 * most] (expert, row0, rows), then their number
+  int most[2];
+  size_t tiles_off[2];
   size_t x_off;         // act [T][H], x read back from an 8-bit checkpoint
   size_t dg_off, du_off, h_off;   // act [P][I]
+  size_t rows_part_off; // float [parts][P][columns]
   size_t dl_off;        // router: float [P]
   size_t part_off;      // router: float [splits][E][H + 1] partial sums (splits > 1)
   int splits;           // router: parts of an expert's rows

@@ -35,14 +35,23 @@ constexpr int kBlockBytes = 128 * kStageBytes;   // 128 rows, or 128 columns, of
 constexpr uint32_t kBufBytes = 0xFFFFFF00u; // no valid offset reaches it
 constexpr uint32_t kNowhere = kBufBytes;    // past every buffer: reads zeros, writes nothing
 
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
 struct TBf16 {
   typedef uint16_t T;
   typedef RowBf16 Row;
   static constexpr int SZ = 2;
   static constexpr int BK = 64;      // k per stage
-  static constexpr int KS = 2;       // MFMA steps per stage
   static __device__ __forceinline__ f32x4_t mma(u32x4_t n, u32x4_t m, f32x4_t c) {
     return mfma_bf16(n, m, c);
+  }
+  // c += ..., in place: the compiler gives an MFMA's result registers of its own,
+  // and 128 accumulators twice do not fit.  It does not see a matrix
+  // instruction here, so what it would wait for is written out: two states
+  // between a vector instruction and an MFMA that reads its result, and, after
+  // the last one, mma_done().
+  static __device__ __forceinline__ void mma32(u32x4_t n, u32x4_t m, f32x16_t& c) {
+    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(n), "v"(m));
   }
   static __device__ __forceinline__ float exp_neg(float g) { return __expf(-g); }
 };
@@ -52,7 +61,6 @@ struct TF32 {
   typedef RowF32 Row;
   static constexpr int SZ = 4;
   static constexpr int BK = 32;
-  static constexpr int KS = 2;
   // four steps of v_mfma_f32_16x16x4_f32; element j of lane group q is k = 4 q + j
   static __device__ __forceinline__ f32x4_t mma(u32x4_t n, u32x4_t m, f32x4_t c) {
 #pragma unroll
@@ -60,13 +68,32 @@ struct TF32 {
       c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(n[j]), __uint_as_float(m[j]), c, 0, 0, 0);
     return c;
   }
+  // four steps of v_mfma_f32_32x32x2_f32; element j of lane half h is k = 4 h + j
+  static __device__ __forceinline__ void mma32(u32x4_t n, u32x4_t m, f32x16_t& c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      asm("s_nop 1\n\tv_mfma_f32_32x32x2_f32 %0, %1, %2, %0" : "+v"(c) : "v"(n[j]), "v"(m[j]));
+  }
   static __device__ __forceinline__ float exp_neg(float g) { return expf(-g); }
 };
+
+// All products of mma32() are done (18 states after the last of 16 passes) and
+// may be read.
+template <int MF, int NF>
+__device__ __forceinline__ void mma_done(f32x16_t (&acc)[MF][NF]) {
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+  for (int t = 0; t < MF; ++t)
+#pragma unroll
+    for (int f = 0; f < NF; ++f) asm volatile("" : "+v"(acc[t][f]));
+}
 
 // A raw buffer as its four words (uniform), for the loads below.
 __device__ __forceinline__ u32x4_t buffer(const void* p) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return u32x4_t{static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32) & 0xffffu, kBufBytes, 0x00020000u};
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
+  return u32x4_t{lo, hi & 0xffffu, kBufBytes, 0x00020000u};
 }
 
 // 64 lanes x 16 (or 4) bytes from the buffer to LDS, lane l's at lds + 16 l (4 l).
@@ -85,6 +112,12 @@ __device__ __forceinline__ void load_lds_word(u32x4_t rs, char* lds, uint32_t of
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS char*)lds)));
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dword %0, %1, 0 offen lds"
                ::"v"(off), "s"(rs), "s"(at) : "memory");
+}
+
+// Rows of expert e within [0, P), whatever the offsets hold.
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int P, int& row0, int& rows) {
+  row0 = min(max(offsets[e], 0), P);
+  rows = min(max(offsets[e + 1], row0), P) - row0;
 }
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
@@ -120,7 +153,8 @@ __device__ __forceinline__ u32x4_t frag_rows_m(const char* s, int m0, int t, int
   return ld16(s + row * kStageBytes + (((q + 4 * ks) ^ key_rows_m(row)) << 4));
 }
 // rows form, N side: fragment f of wave wn of NW: row 32 wn + 8 (i / 4) + 4 (f % 2) + i % 4 of
-// gate (f < 2) or of up, behind the 32 NW rows of gate
+// gate (f < 2) or of up, behind the 32 NW rows of gate; a result lane has 8
+// neighbouring ones
 template <int NW>
 __device__ __forceinline__ u32x4_t frag_rows_n(const char* s, int wn, int f, int ks, int lane) {
   const int i = lane & 15, q = lane >> 4;
@@ -156,6 +190,47 @@ __device__ __forceinline__ u32x4_t frag_cols(const char* s, int half, int f, int
   }
 }
 
+// Fragments of the 32 x 32 products (16 bf16 or 8 float32 of k a step): lane i =
+// lane % 32 holds one index, lane half h = lane / 32 the k.  A result lane (i, h)
+// has row i and column indexes 8 g + 4 h + j; index 8 g + 4 h + j is column 16 h + 4 g + j, so
+// that it has 16 neighbouring columns.
+__device__ __forceinline__ int col_of_index(int i) { return 16 * ((i >> 2) & 1) + 4 * (i >> 3) + (i & 3); }
+
+__device__ __forceinline__ int key32_rows_n(int row) { return ((row >> 1) & 3) | (((row >> 4) & 1) << 2); }
+template <class E>
+__device__ __forceinline__ int key32_cols(int k) {
+  return E::SZ == 2 ? (k & 3) << 2 : ((k >> 2) & 1) << 3;
+}
+// rows form
+__device__ __forceinline__ u32x4_t frag32_rows_m(const char* s, int row0, int ks, int lane) {
+  const int row = row0 + (lane & 31);
+  return ld16(s + row * kStageBytes + (((2 * ks + (lane >> 5)) ^ key_rows_m(row)) << 4));
+}
+__device__ __forceinline__ u32x4_t frag32_rows_n(const char* s, int row0, int ks, int lane) {
+  const int row = row0 + col_of_index(lane & 31);
+  return ld16(s + row * kStageBytes + (((2 * ks + (lane >> 5)) ^ key32_rows_n(row)) << 4));
+}
+// columns form, columns col0 .. + 31 of a block of 128: in index order (N side) or as they lie (M side)
+template <class E, bool N>
+__device__ __forceinline__ u32x4_t frag32_cols(const char* s, int col0, int ks, int lane) {
+  const int h = lane >> 5;
+  if constexpr (E::SZ == 2) {
+    const int c = lane & 3, second = (lane >> 4) & 1, k = 16 * ks + 8 * h + ((lane & 15) >> 2);
+    // first column of this lane's 8 bytes
+    const int col = col0 + (N ? 16 * (c & 1) + 4 * (2 * second + (c >> 1)) : 16 * second + 4 * c);
+    const char* p = s + k * 256 + (((col >> 3) ^ key32_cols<E>(k)) << 4) + 2 * (col & 4);
+    const u32x2_t lo = lds_transposed(p), hi = lds_transposed(p + 4 * 256);
+    return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+  } else {
+    const int k = 8 * ks + 4 * h, col = col0 + (N ? col_of_index(lane & 31) : lane & 31);
+    const char* p = s + k * 512 + (((col >> 2) ^ key32_cols<E>(k)) << 4) + 4 * (col & 3);
+    u32x4_t v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(p + j * 512);
+    return v;
+  }
+}
+
 // A lane's results of a row: fragment f holds columns 16 f + 4 q .. + 3.  Exchanging
 // fragments f and f + 1 between lane groups q and q ^ 1 leaves each lane with 8
 // neighbouring columns, pair_col(f / 2) .. + 7, of the 32.
@@ -178,6 +253,23 @@ __device__ __forceinline__ void pair_vals(const f32x4_t (&a)[4], int pair, float
   }
 }
 
+// Division by the number of slots: p / k = (t + ((p - t) >> 1)) >> s with t = high word of
+// p m, m = floor(2^32 (2^(s + 1) - k) / k) + 1, 2^s < k <= 2^(s + 1), for any 32-bit p.
+struct PairDiv {
+  uint32_t k, m, s;
+  static PairDiv of(int k) {
+    PairDiv d{static_cast<uint32_t>(k), 0, 0};
+    while ((uint64_t{2} << d.s) < d.k) ++d.s;
+    d.m = static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{2} << d.s) - d.k)) / d.k + 1);
+    return d;
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t p) const {
+    if (k == 1) return p;
+    const uint32_t t = __umulhi(p, m);
+    return (t + ((p - t) >> 1)) >> s;
+  }
+};
+
 // This wave's loads into LDS but for the `YOUNGER` memory operations issued
 // after them are done, and so, behind the barrier, are those of all waves; all
 // LDS reads before it are done too.  Memory operations count in order of issue.
@@ -189,23 +281,17 @@ __device__ __forceinline__ void stage_barrier() {
 // Keeps instructions on either side apart.
 __device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
 
-// What one MFMA step reads from LDS.
-template <int MF>
-struct Frags {
-  u32x4_t n[4], m[MF];
-};
-
-// Main loop over a ring of R stages in LDS, GROUP loads a wave and stage.  The
-// fragments of a step are read while the step before it is multiplied, so LDS
-// and the matrix cores work at the same time (reads and products in turn, by
-// all waves together behind each barrier, took 1.4 times as long).  The barrier
-// of stage s stands between its two steps: behind it the loads of stage s + 1
-// have landed and all of stage s has been read, so stage s + R goes into its
-// place at once.
+// Main loop over a ring of R stages in LDS, KS steps and GROUP loads of a wave
+// each.  The fragments of a step are read while the step before it is
+// multiplied, so LDS and the matrix cores work at the same time.  The barrier
+// of stage s stands before its last step's products: behind it the loads of
+// stage s + 1 have landed and all of stage s has been read, so stage s + R goes
+// into its place at once.
 //   issue(s, stage): starts the loads of stage s;  read(stage, ks, frags);  mma(frags)
-template <int R, int GROUP, class F, class Issue, class Read, class Mma>
+template <int R, int KS, int GROUP, class F, class Issue, class Read, class Mma>
 __device__ __forceinline__ void ring_loop(int stages, char* ring, int bytes, F& even, F& odd, Issue&& issue,
                                           Read&& read, Mma&& mma) {
+  static_assert(KS % 2 == 0, "steps take the fragments in turn");
   if (stages <= 0) return;
 #pragma unroll
   for (int s = 0; s < R; ++s)
@@ -216,13 +302,18 @@ __device__ __forceinline__ void ring_loop(int stages, char* ring, int bytes, F& 
     stage_barrier<0>();
   read(ring, 0, even);
   int now = 0;   // offset of stage s
-  for (int s = 0;; ++s) {
-    read(ring + now, 1, odd);
-    sched_fence();
-    mma(even);
-    if (s + 1 == stages) break;
+  const auto steps = [&] {   // all but the last one's products
+#pragma unroll
+    for (int ks = 0; ks + 1 < KS; ++ks) {
+      read(ring + now, ks + 1, ks & 1 ? even : odd);
+      sched_fence();
+      mma(ks & 1 ? odd : even);
+      sched_fence();
+    }
+  };
+  for (int s = 0; s + 1 < stages; ++s) {
+    steps();
     const int next = now == (R - 1) * bytes ? 0 : now + bytes;
-    sched_fence();
     if (s + R - 1 < stages)
       stage_barrier<GROUP * (R - 2)>();
     else
@@ -233,6 +324,7 @@ __device__ __forceinline__ void ring_loop(int stages, char* ring, int bytes, F& 
     mma(odd);
     now = next;
   }
+  steps();
   mma(odd);
 }
 

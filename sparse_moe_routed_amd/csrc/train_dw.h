@@ -1,0 +1,21 @@
+// Arguments of the weight gradients' kernels.
+#pragma once
+
+#include "moe_internal.h"
+#include "train_rows.h"
+
+namespace moe {
+
+struct DwArgs {
+  const void *dg, *du, *h, *dy, *x;
+  void *dgate, *dup, *ddown;
+  const int32_t *offsets, *sorted_pair;
+  PairDiv slots;
+  int E, H, I, P;
+  int strip;   // neighbouring tiles of a workgroup
+  int unit;    // neighbouring strips on one XCD
+};
+
+hipError_t launch_dw(const moe_shape& s, const DwArgs& a, hipStream_t st);
+
+}  // namespace moe

@@ -95,10 +95,11 @@ void sizes() {
                 continue;
               }
               const size_t P = static_cast<size_t>(T) * k, a = act == MOE_DT_F32 ? 4 : 2;
-              EXPECT(n >= 3 * P * I * a + static_cast<size_t>(T) * H * a + P * 4, 1);
+              EXPECT(n >= 3 * P * I * a + static_cast<size_t>(T) * H * a, 1);
               moe::TrainPlan pl;
               moe::make_train_plan(s, &pl);
-              EXPECT(pl.max_tiles >= 1 && pl.bm >= 1, 1);
+              for (const moe::RowCut& c : {pl.gate_up, pl.dh, pl.dx}) EXPECT(c.shape >= 0 && c.shape <= 2 && c.parts >= 1, 1);
+              EXPECT(pl.most[0] >= 1 && pl.most[1] >= 1, 1);
               (void)moe::train_fits(s, pl);
             }
 }

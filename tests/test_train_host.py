@@ -208,7 +208,7 @@ def test_empty_batch():
 def test_workspace_size_covers_its_regions():
     s = shape(T=512, H=2560, E=512, I=640, top_k=10)
     P = 512 * 10
-    assert M.moe_train_workspace_size(s) >= 3 * P * 640 * 2 + 512 * 2560 * 2 + P * 4
+    assert M.moe_train_workspace_size(s) >= 3 * P * 640 * 2 + 512 * 2560 * 2
     # any valid shape has one: the router's gradient takes every weight format
     assert M.moe_train_workspace_size(shape(wfmt="int2_g32")) > 0
     assert M.moe_train_workspace_size(shape(I=128, flags=M.MOE_F_TILED_WEIGHTS)) > 0
