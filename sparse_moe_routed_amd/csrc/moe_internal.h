@@ -212,8 +212,6 @@ struct TrainPlan {
   size_t dg_off, du_off, h_off;   // act [P][I]
   size_t rows_part_off; // float [parts][P][columns]
   size_t dl_off;        // router: float [P]
-  size_t part_off;      // router: float [splits][E][H + 1] partial sums (splits > 1)
-  int splits;           // router: parts of an expert's rows
   size_t total;
 };
 void make_train_plan(const moe_shape& s, TrainPlan* p);
@@ -236,9 +234,8 @@ struct RouterBwd {
   const void *x, *w_router, *dx_in;
   const int32_t *offsets, *sorted_pair;
   void* dx;
-  float *dw_router, *dbias, *dl, *part;
+  float *dw_router, *dbias, *dl;
 };
-hipError_t launch_router_bwd(const moe_shape& s, const TrainPlan& pl, const RouterBwd& a,
-                             hipStream_t st);
+hipError_t launch_router_bwd(const moe_shape& s, const RouterBwd& a, hipStream_t st);
 
 }  // namespace moe

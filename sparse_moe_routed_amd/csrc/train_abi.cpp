@@ -213,7 +213,7 @@ int moe_router_backward(const moe_shape* shape, const int32_t* topk_ids, const f
     if (!sums) return MOE_OK;
     if (any_alias(outs, 3, nullptr, 0)) return MOE_E_ALIAS;
     (void)hipGetLastError();
-    return device_status(launch_router_bwd(s, pl, r, stream));
+    return device_status(launch_router_bwd(s, r, stream));
   }
   if ((st = check_ptrs({topk_ids, topk_w, dw}))) return st;
   if ((dx && !w_router) || (dw_router && !x)) return MOE_E_NULL;
@@ -242,9 +242,8 @@ int moe_router_backward(const moe_shape* shape, const int32_t* topk_ids, const f
   r.dx_in = dx_in;
   r.dx = dx;
   r.dl = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.dl_off);
-  r.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.part_off);
   (void)hipGetLastError();
-  return device_status(launch_router_bwd(s, pl, r, stream));
+  return device_status(launch_router_bwd(s, r, stream));
 }
 
 }  // extern "C"

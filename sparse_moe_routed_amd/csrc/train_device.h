@@ -81,6 +81,11 @@ struct TF32 {
 // may be read.
 template <int MF, int NF>
 __device__ __forceinline__ void mma_done(f32x16_t (&acc)[MF][NF]) {
+  // every product is issued before the waits, every reader stays behind them
+#pragma unroll
+  for (int t = 0; t < MF; ++t)
+#pragma unroll
+    for (int f = 0; f < NF; ++f) asm volatile("" : "+v"(acc[t][f]));
   asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 #pragma unroll
   for (int t = 0; t < MF; ++t)

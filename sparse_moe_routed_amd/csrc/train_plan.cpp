@@ -57,7 +57,6 @@ static RowCut best_cut(const moe_shape& s, int columns, int depth, bool half, bo
 void make_train_plan(const moe_shape& s, TrainPlan* p) {
   const size_t P = static_cast<size_t>(s.T) * s.top_k, a = act_bytes(s);
   *p = TrainPlan{};
-  p->splits = 1;
   if (s.T == 0) return;
   p->gate_up = best_cut(s, s.I, s.H, true, true);
   // its loads and stores after the sum weigh more than what taller tiles save
@@ -85,7 +84,6 @@ void make_train_plan(const moe_shape& s, TrainPlan* p) {
   const size_t products = at;
   at = 0;
   p->dl_off = take(P * 4);
-  p->part_off = take(p->splits > 1 ? static_cast<size_t>(p->splits) * s.E * (s.H + 1) * 4 : 0);
   p->total = std::max(products, at);
 }
 

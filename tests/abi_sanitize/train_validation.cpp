@@ -31,7 +31,7 @@ hipError_t launch_ffn_backward(const moe_shape&, const TrainPlan&, const void*, 
                                void*, const moe_experts*, void*, hipStream_t) {
   reached("launch_ffn_backward");
 }
-hipError_t launch_router_bwd(const moe_shape&, const TrainPlan&, const RouterBwd&, hipStream_t) {
+hipError_t launch_router_bwd(const moe_shape&, const RouterBwd&, hipStream_t) {
   reached("launch_router_bwd");
 }
 
