@@ -78,16 +78,23 @@ static hipError_t launch_tiles(const moe_shape& s, const TrainPlan& pl, const mo
   return hipGetLastError();
 }
 
+// f(shape) of a cut.  Where an expert's rows are about one tile, a weight is read
+// about once.
+template <bool WIDE, class F>
+static hipError_t with_shape(const moe_shape& s, const RowCut& c, F&& f) {
+  const bool once = static_cast<int64_t>(s.T) * s.top_k <= static_cast<int64_t>(s.E) * row_height(c.shape);
+  if constexpr (WIDE)
+    if (c.shape == kRowsWide) return f(Wide{});
+  if (c.shape == kRowsFew) return once ? f(FewOnce{}) : f(Few{});
+  return once ? f(ManyOnce{}) : f(Many{});
+}
+
 template <class E>
 static hipError_t gate_up(const moe_shape& s, const TrainPlan& pl, const void* x, const moe_experts& ex,
                           const moe_perm& pm, const moe_saved& sv, void* h, void* ws, hipStream_t st) {
   const RowArgs a = row_args(s, pl, pm, ws, pl.gate_up);
   const GateUpOut o{sv.g, sv.u, h, sv.g_scale, sv.u_scale};
-  switch (pl.gate_up.shape) {
-    case kRowsFew: return run_gate_up<E, Few>(a, x, ex, o, st);
-    case kRowsMany: return run_gate_up<E, Many>(a, x, ex, o, st);
-    default: return run_gate_up<E, Wide>(a, x, ex, o, st);
-  }
+  return with_shape<true>(s, pl.gate_up, [&](auto shape) { return run_gate_up<E, decltype(shape)>(a, x, ex, o, st); });
 }
 
 hipError_t launch_gate_up_save(const moe_shape& s, const TrainPlan& pl, const void* x,
@@ -103,14 +110,10 @@ template <class E>
 static hipError_t rows_backward(const moe_shape& s, const TrainPlan& pl, const void* dy, const DhArgs& d,
                                 const moe_experts& ex, const moe_perm& pm, void* drows, void* ws, hipStream_t st) {
   const RowArgs a = row_args(s, pl, pm, ws, pl.dh), b = row_args(s, pl, pm, ws, pl.dx);
-  const hipError_t e = pl.dh.shape == kRowsFew ? run_dh<E, Few>(a, dy, ex.down, d, st)
-                                               : run_dh<E, Many>(a, dy, ex.down, d, st);
+  const hipError_t e =
+      with_shape<false>(s, pl.dh, [&](auto shape) { return run_dh<E, decltype(shape)>(a, dy, ex.down, d, st); });
   if (e != hipSuccess || !drows) return e;
-  switch (pl.dx.shape) {
-    case kRowsFew: return run_dx<E, Few>(b, d, ex, drows, st);
-    case kRowsMany: return run_dx<E, Many>(b, d, ex, drows, st);
-    default: return run_dx<E, Wide>(b, d, ex, drows, st);
-  }
+  return with_shape<true>(s, pl.dx, [&](auto shape) { return run_dx<E, decltype(shape)>(b, d, ex, drows, st); });
 }
 
 hipError_t launch_ffn_backward(const moe_shape& s, const TrainPlan& plan, const void* dy,
@@ -149,6 +152,8 @@ hipError_t launch_ffn_backward(const moe_shape& s, const TrainPlan& plan, const 
     a.slots = PairDiv::of(s.top_k);
   }
   if (!dex) return hipSuccess;
+  a.parts = pl.dw_parts;
+  a.part = at_off<float>(ws, pl.dw_part_off);
   a.dy = dy;
   a.x = x;
   a.dgate = const_cast<void*>(dex->gate);

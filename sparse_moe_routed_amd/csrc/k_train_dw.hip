@@ -2,6 +2,7 @@
 // dW_down = dy^T h, each a sum over the expert's rows.  Both sides of these
 // products have their output index contiguous in memory.
 #include <algorithm>
+#include <type_traits>
 
 #include "train_dw.h"
 
@@ -13,17 +14,25 @@ namespace moe {
 // in columns form, with the expert's rows as k.
 //
 // An expert of at most two stages of rows keeps its M side in registers for the
-// whole strip, and only the N side runs through a ring (three stages ahead); with more rows
-// both sides run through a ring of two.  Either way the stages of all tiles are
-// one pipeline, so the next loads are on their way while a tile is stored.
-template <class E>
+// whole strip, and only the N side runs through LDS, step by step of half a
+// stage; with more rows both sides run through a ring of two stages.  Either way
+// the steps of all tiles are one pipeline, so the next loads are on their way
+// while a tile is stored.  PART: float32 sums of a part of the rows.
+//
+// Bound by the stores: 512 experts of 2560 x 640 are 5.0 GB of gradients, at five
+// rows each 920 us, at 80 skewed ones 1250 (there reads of x, dy and h that miss
+// L2, 1.35 GB, compete with them).  Stores of whole cache lines that leave the
+// caches first took 1600 us to 1290, steps of half a stage seven deep the five rows
+// from 1100 to 1010.
+template <class E, bool PART>
 struct DwStrip {
   typedef Shape<2, 2, 4, 2, 16> S;
+  typedef std::conditional_t<PART, TF32, E> Out;
   static constexpr int LOADS = 4;                     // of a wave, side and stage
   static constexpr int KR = E::SZ == 2 ? 4 : 2;       // k rows of a load
-  static constexpr int PAIR_BYTES = 256;             // of a wave and stage
+  static constexpr int PAIR_BYTES = 256;              // of a wave and stage
   static constexpr int LDS = 4 * kBlockBytes + 4 * S::WAVES * PAIR_BYTES;
-  static constexpr int STORES = 4 * 16 * E::SZ / 16;  // of a thread and tile
+  static constexpr int STORES = 4 * 16 * Out::SZ / 16;   // of a thread and tile
 
   const DwArgs& a;
   char* lds;
@@ -40,7 +49,7 @@ struct DwStrip {
 
   __device__ __forceinline__ DwStrip(const DwArgs& args, char* shared) : a(args), lds(shared) {}
 
-  __device__ __forceinline__ void init(int e, int which, int mt, int first, int count) {
+  __device__ __forceinline__ void init(int part, int e, int which, int mt, int first, int count) {
     const bool down = which == 2;
     gather = !down;
     mcols = down ? a.H : a.I;
@@ -50,6 +59,11 @@ struct DwStrip {
     tiles = count;
     row0 = rows = 0;
     if (a.P > 0) expert_rows(a.offsets, e, a.P, row0, rows);
+    if constexpr (PART) {
+      const int per = (rows + E::BK * a.parts - 1) / (E::BK * a.parts) * E::BK;
+      row0 += min(part * per, rows);
+      rows = min(max(rows - part * per, 0), per);
+    }
     row0 = __builtin_amdgcn_readfirstlane(row0);
     rows = __builtin_amdgcn_readfirstlane(rows);
     stages = (rows + E::BK - 1) / E::BK;
@@ -57,35 +71,32 @@ struct DwStrip {
             (static_cast<size_t>(row0) * mcols + m0) * E::SZ;
     nside = down ? static_cast<const char*>(a.h) + static_cast<size_t>(row0) * a.I * E::SZ
                  : static_cast<const char*>(a.x);
-    out = static_cast<char*>(down ? a.ddown : which ? a.dup : a.dgate) +
-          (static_cast<size_t>(e) * a.I * a.H + static_cast<size_t>(m0) * ncols) * E::SZ;
+    const size_t whole = static_cast<size_t>(a.I) * a.H, at = static_cast<size_t>(m0) * ncols;
+    if constexpr (PART)
+      out = reinterpret_cast<char*>(a.part + (static_cast<size_t>(part * 3 + which) * a.E + e) * whole + at);
+    else
+      out = static_cast<char*>(down ? a.ddown : which ? a.dup : a.dgate) + (e * whole + at) * E::SZ;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
       krow[j] = cols_k<E>(j * S::WAVES + T.w, T.lane);
       chunk[j] = (cols_pos<E>(T.lane) ^ key_cols<E>(krow[j])) * (16 / E::SZ);
     }
-    // The gathered rows' pairs go through LDS too; every wave loads those of its
-    // own k rows (lane 8 j + i: row i of load j).  Those of loads n are requested
-    // with loads n - 3: loads n are issued when loads n - 3 (few rows) or later
-    // ones (many rows) are known to have landed.
+    // Many rows: the gathered rows' pairs go through LDS too; every wave loads
+    // those of its own k rows (lane 8 j + i: row i of load j), with loads n those
+    // of loads n + 3.
     pair_rs = buffer(a.sorted_pair + row0);
     pair_lds = lds + 4 * kBlockBytes + T.w * PAIR_BYTES;
     pair_row = cols_k<E>(((T.lane >> 3) & 3) * S::WAVES + T.w, 0) + (T.lane & (KR - 1));
   }
 
   __device__ __forceinline__ void store_tile(int nt) {
-    const char* tile = out + static_cast<size_t>(nt) * 128 * E::SZ;
+    const char* tile = out + static_cast<size_t>(nt) * 128 * Out::SZ;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int r = T.row(t);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        float v[8];
-        pair_vals(T.acc[t], p, v);
-        const int c = T.col(p);
-        store_vals<E>(tile, nt * 128 + c < ncols && m0 + r < mcols ? static_cast<uint32_t>(r * ncols + c) * E::SZ : kNowhere, v);
-      }
-    }
+    for (int t = 0; t < 4; ++t)
+      line_pieces<Out>(T.acc[t], T.lane, [&](int row, int col, u32x4_t v) {
+        const int r = 64 * T.wm + 16 * t + row, c = 64 * T.wn + col;
+        store_piece(tile, nt * 128 + c < ncols && m0 + r < mcols ? static_cast<uint32_t>(r * ncols + c) * Out::SZ : kNowhere, v);
+      });
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -154,122 +165,155 @@ struct DwStrip {
       for (int f = 0; f < 4; ++f) T.acc[t][f] = E::mma(n[f], m[t], T.acc[t][f]);
   }
 
-  // at most two stages of rows
+  // At most STEPS (one to four) steps of rows, half a stage each.  The N side's
+  // steps of all tiles run through a ring of eight, seven loaded ahead.
+  template <int STEPS>
   __device__ __forceinline__ void run_few() {
-    u32x4_t m[2][2][4];   // stage, step
-    first_pairs();
+    constexpr int BYTES = kBlockBytes / 2, RING = 8, AHEAD = RING - 1, PER = LOADS / 2, K = E::BK / 2;
+    u32x4_t m[STEPS][4];
     issue_m(0, lds);
-    if (stages > 1) issue_m(1, lds + kBlockBytes);
+    if (STEPS > 2) issue_m(1, lds + kBlockBytes);
+    uint32_t off[STEPS][PER];   // byte offset of a lane's 16 bytes within the tile's columns
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int k = s * K + krow[j];
+        uint32_t row = k;
+        if (gather) row = a.slots.div(min(max(a.sorted_pair[row0 + min(k, rows - 1)], 0), a.P - 1));
+        off[s][j] = k < rows ? row * static_cast<uint32_t>(ncols * E::SZ) + static_cast<uint32_t>(chunk[j] * E::SZ) : kNowhere;
+      }
     stage_barrier<0>();
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-      if (s < stages) {
-        read_m(lds + s * kBlockBytes, 0, m[s][0]);
-        read_m(lds + s * kBlockBytes, 1, m[s][1]);
-      }
+    for (int s = 0; s < STEPS; ++s) read_m(lds + s * BYTES, 0, m[s]);
     stage_barrier<0>();   // all waves have read
-    constexpr int GROUP = LOADS + 1;
+    const int limit = min(ncols, (nt0 + tiles) * 128);   // behind the strip: loads of zeros, to keep count
+    const auto issue = [&](int tile, int s, int slot) {
+      const int n0 = (nt0 + tile) * 128;
+      const u32x4_t rn = buffer(nside + static_cast<size_t>(n0) * E::SZ);
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (lt < tiles) issue_n(lds + i * kBlockBytes);
+      for (int j = 0; j < PER; ++j)
+        load_lds(rn, lds + (slot & (RING - 1)) * BYTES + (j * S::WAVES + T.w) * 1024,
+                 n0 + chunk[j] < limit ? off[s][j] : kNowhere);
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) issue(i / STEPS, i % STEPS, i);
     int slot = 0;
     for (int t = 0; t < tiles; ++t) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s >= stages) break;
-        // This stage's loads are done.  Younger are those of the two after it and the stores
-        // since the third stage before it: those of three tiles of one stage, of one or two of two.
-        const int stores = stages == 1 ? t : min(t, 1);
-        if (lt == tiles || stores == 0)
-          lt == tiles ? stage_barrier<0>() : stage_barrier<2 * GROUP>();
-        else if (stores < 3)
-          stage_barrier<2 * GROUP + STORES>();
-        else
-          stage_barrier<2 * GROUP + 3 * STORES>();
-        // all waves have read the stage before it
-        if (lt < tiles) issue_n(lds + ((slot + 3) & 3) * kBlockBytes);
-        const char* st = lds + slot * kBlockBytes;
-        u32x4_t n0[4], n1[4];
-        read_n(st, 0, n0);
-        read_n(st, 1, n1);
-        mma(n0, m[s][0]);
-        mma(n1, m[s][1]);
-        slot = (slot + 1) & 3;
+      for (int s = 0; s < STEPS; ++s) {
+        // This step's loads are done.  Younger are the six after it and the stores of the
+        // tiles that ended since they were issued (of all of them or, where a wave's
+        // count ends, the last ones).
+        constexpr int MOST = (63 - (AHEAD - 1) * PER) / STORES;
+        const int stores = std::min((AHEAD - s + STEPS - 1) / STEPS, MOST);
+        younger<(AHEAD - 1) * PER>(t < stores ? 0 : stores);
+        // all waves have read the step before it
+        issue(t + (s + AHEAD) / STEPS, (s + AHEAD) % STEPS, slot + AHEAD);
+        u32x4_t n[4];
+        read_n(lds + (slot & (RING - 1)) * BYTES, 0, n);
+        mma(n, m[s]);
+        ++slot;
       }
       store_tile(nt0 + t);
     }
   }
+  template <int LOADED>
+  static __device__ __forceinline__ void younger(int tiles_stored) {
+    switch (tiles_stored) {
+      case 0: return stage_barrier<LOADED>();
+      case 1: return stage_barrier<LOADED + STORES>();
+      case 2: return stage_barrier<LOADED + 2 * STORES>();
+      case 3: return stage_barrier<LOADED + 3 * STORES>();
+      case 4: return stage_barrier<std::min(63, LOADED + 4 * STORES)>();
+      case 5: return stage_barrier<std::min(63, LOADED + 5 * STORES)>();
+      default: return stage_barrier<std::min(63, LOADED + 6 * STORES)>();
+    }
+  }
 
+  // More rows.  The other workgroup of the CU fills the time of this one's reads.
   __device__ __forceinline__ void run_many() {
-    constexpr int GROUP = 2 * LOADS + 1;
     const auto issue = [&](char* st) {
       issue_m(ls, st + kBlockBytes);
       issue_n(st);
     };
     first_pairs();
     issue(lds);
-    if (lt < tiles) issue(lds + 2 * kBlockBytes);
-    if (ln == 2)
-      stage_barrier<GROUP>();
-    else
-      stage_barrier<0>();
-    u32x4_t n[2][4], m[2][4];   // step
-    read_n(lds, 0, n[0]);
-    read_m(lds + kBlockBytes, 0, m[0]);
-    int now = 0, s = 0;
-    bool stored = false;
-    for (int nt = nt0, left = tiles * stages;; --left) {
-      read_n(lds + now, 1, n[1]);
-      read_m(lds + now + kBlockBytes, 1, m[1]);
-      sched_fence();
-      mma(n[0], m[0]);
-      if (left == 1) break;
-      const int next = now ^ (2 * kBlockBytes);
-      sched_fence();
-      if (stored)
-        stage_barrier<STORES>();
-      else
-        stage_barrier<0>();
-      if (lt < tiles) issue(lds + now);
-      read_n(lds + next, 0, n[0]);
-      read_m(lds + next + kBlockBytes, 0, m[0]);
-      sched_fence();
-      mma(n[1], m[1]);
-      now = next;
-      stored = ++s == stages;
-      if (stored) {
-        store_tile(nt++);
-        s = 0;
+    int now = 0;
+    for (int t = 0; t < tiles; ++t) {
+      for (int s = 0; s < stages; ++s) {
+        // younger than this stage's loads: the stores of the tile before
+        if (t > 0 && s == 0)
+          stage_barrier<STORES>();
+        else
+          stage_barrier<0>();
+        // all waves have read the stage before it
+        if (lt < tiles) issue(lds + (now ^ (2 * kBlockBytes)));
+        const char* st = lds + now;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          u32x4_t n[4], m[4];
+          read_n(st, ks, n);
+          read_m(st + kBlockBytes, ks, m);
+          mma(n, m);
+        }
+        now ^= 2 * kBlockBytes;
       }
+      store_tile(nt0 + t);
     }
-    mma(n[1], m[1]);
-    store_tile(nt0 + tiles - 1);
   }
 };
 
-template <class E>
+template <class E, bool PART>
 __global__ __launch_bounds__(256, 2) void k_dw(DwArgs a) {
-  __shared__ __align__(16) char lds[DwStrip<E>::LDS];
+  __shared__ __align__(16) char lds[DwStrip<E, PART>::LDS];
   const int it = (a.I + 127) / 128, ht = a.H / 128;
   const int wide = it * ((ht + a.strip - 1) / a.strip), tall = ht * ((it + a.strip - 1) / a.strip);
   const int each = 2 * wide + tall;
   // strips are dealt to the XCDs in units (workgroups in turn)
   const int turn = static_cast<int>(blockIdx.x >> 3), unit = turn / a.unit;
-  const int item = (unit * 8 + static_cast<int>(blockIdx.x & 7)) * a.unit + turn - unit * a.unit;
-  if (item >= each * a.E) return;
+  int item = (unit * 8 + static_cast<int>(blockIdx.x & 7)) * a.unit + turn - unit * a.unit, part = 0;
+  if (item >= each * a.E * (PART ? a.parts : 1)) return;
+  if constexpr (PART) {
+    part = item / (each * a.E);
+    item -= part * each * a.E;
+  }
   const int e = item / each, in_e = item - e * each;
   const int which = in_e < wide ? 0 : in_e < 2 * wide ? 1 : 2, ntiles = which == 2 ? it : ht;
   const int strips = (ntiles + a.strip - 1) / a.strip, b = in_e - which * wide;
   const int mt = b / strips, nt0 = (b - mt * strips) * a.strip;
-  DwStrip<E> s(a, lds);
-  s.init(e, which, mt, nt0, min(a.strip, ntiles - nt0));
-  if (s.rows == 0) {
-    for (int t = 0; t < s.tiles; ++t) s.store_tile(nt0 + t);
-  } else if (s.stages <= 2) {
-    s.run_few();
-  } else {
-    s.run_many();
+  DwStrip<E, PART> s(a, lds);
+  s.init(part, e, which, mt, nt0, min(a.strip, ntiles - nt0));
+  switch ((s.rows + E::BK / 2 - 1) / (E::BK / 2)) {
+    case 0:
+      for (int t = 0; t < s.tiles; ++t) s.store_tile(nt0 + t);
+      break;
+    case 1: s.template run_few<1>(); break;
+    case 2: s.template run_few<2>(); break;
+    case 3: s.template run_few<3>(); break;
+    case 4: s.template run_few<4>(); break;
+    default: s.run_many();
   }
+}
+
+// Joins the parts of all three gradients, eight values a thread.
+template <class E>
+__global__ __launch_bounds__(256) void k_join_dw(DwArgs a) {
+  const size_t each = static_cast<size_t>(a.E) * a.I * a.H;
+  const size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= 3 * each) return;
+  float v[8] = {};
+  for (int p = 0; p < a.parts; ++p) {
+    const float* q = a.part + p * 3 * each + i;
+    const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(q), hi = *reinterpret_cast<const f32x4_t*>(q + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] += lo[j];
+      v[4 + j] += hi[j];
+    }
+  }
+  const size_t which = i / each;
+  store_vals<E>(static_cast<typename E::T*>(which == 2 ? a.ddown : which ? a.dup : a.dgate) + (i - which * each), v);
 }
 
 // Many rows per expert: one tile of 256 x 256 by eight waves, both sides through a
@@ -366,16 +410,24 @@ constexpr int kMaxStrip = 20;
 template <class E>
 static hipError_t run(const moe_shape& s, DwArgs a, hipStream_t st) {
   const auto up = [](int v, int d) { return (v + d - 1) / d; };
-  if (a.P / s.E >= 512) {
+  if (a.parts == 0) {
     const int total = 3 * s.E * up(s.I, Wide::BM) * up(s.H, Wide::BM);
     k_dw_wide<E><<<up(total, 8) * 8, Wide::THREADS, 0, st>>>(a);
     return hipGetLastError();
   }
   const int it = up(s.I, 128), ht = s.H / 128;
   a.strip = std::min(std::max(3 * s.E * it * ht / 4096, 1), kMaxStrip);
-  const int each = 2 * it * up(ht, a.strip) + ht * up(it, a.strip), strips = s.E * each;
+  const int each = 2 * it * up(ht, a.strip) + ht * up(it, a.strip), strips = s.E * each * a.parts;
   a.unit = std::max(1, std::min(each, strips / 64));
-  k_dw<E><<<up(strips, 8 * a.unit) * 8 * a.unit, 256, 0, st>>>(a);
+  const int grid = up(strips, 8 * a.unit) * 8 * a.unit;
+  if (a.parts > 1) {
+    k_dw<E, true><<<grid, 256, 0, st>>>(a);
+    if (const hipError_t e = hipGetLastError()) return e;
+    const size_t threads = static_cast<size_t>(3) * s.E * s.I * s.H / 8;
+    k_join_dw<E><<<static_cast<int>((threads + 255) / 256), 256, 0, st>>>(a);
+  } else {
+    k_dw<E, false><<<grid, 256, 0, st>>>(a);
+  }
   return hipGetLastError();
 }
 

@@ -205,12 +205,14 @@ constexpr int kLookupExperts = 64;   // up to here a wave finds its tile itself
 // gradient overlap, as no call uses both.
 struct TrainPlan {
   RowCut gate_up, dh, dx;
+  int dw_parts;   // parts of an expert's rows in the weight gradients, 0: by 256 x 256 tiles
   // tile lists, by row height 32 or 128 / 256: int32 [3 * most] (expert, row0, rows), then their number
   int most[2];
   size_t tiles_off[2];
   size_t x_off;         // act [T][H], x read back from an 8-bit checkpoint
   size_t dg_off, du_off, h_off;   // act [P][I]
   size_t rows_part_off; // float [parts][P][columns]
+  size_t dw_part_off;   // float [dw_parts][3][E][I H]
   size_t dl_off;        // router: float [P]
   size_t total;
 };

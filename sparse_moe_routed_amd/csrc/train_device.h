@@ -108,10 +108,18 @@ __device__ __forceinline__ u32x4_t buffer(const void* p) {
 // and the registers are read when the load is issued.  The five wait states in
 // front are what a buffer load needs after the vector unit has written one
 // of its scalar registers.
+// ONCE: data that is read about once leaves the caches first (256 tokens, 512 experts of
+// 2560 x 640: dh 330 -> 270 us, dx 570 -> 520; where weights are read again, at
+// 8192 rows of one expert, it costs: 335 -> 356).
+template <bool ONCE = false>
 __device__ __forceinline__ void load_lds(u32x4_t rs, char* lds, uint32_t off) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS char*)lds)));
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-               ::"v"(off), "s"(rs), "s"(at) : "memory");
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds"
+                 ::"v"(off), "s"(rs), "s"(at) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 ::"v"(off), "s"(rs), "s"(at) : "memory");
 }
 __device__ __forceinline__ void load_lds_word(u32x4_t rs, char* lds, uint32_t off) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS char*)lds)));
@@ -258,6 +266,43 @@ __device__ __forceinline__ void pair_vals(const f32x4_t (&a)[4], int pair, float
   }
 }
 
+// Lanes 8 .. 15 of each 16 of `a` against lanes 0 .. 7 of `b`.  Where a lane i holds
+// a piece of row i, `a` is left with two pieces each of rows 0 .. 7, in lanes i and
+// i + 8, and `b` with those of rows 8 .. 15.
+__device__ __forceinline__ void swap_rows(u32x4_t& a, u32x4_t& b) {
+  constexpr int kRor8 = 0x128;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int x = static_cast<int>(a[j]), y = static_cast<int>(b[j]);
+    a[j] = __builtin_amdgcn_update_dpp(x, y, kRor8, 0xF, 0xC, false);
+    b[j] = __builtin_amdgcn_update_dpp(y, x, kRor8, 0xF, 0x3, false);
+  }
+}
+
+// Results a[4] of 16 rows and 64 columns as stores of whole cache lines (128 bytes):
+// f(row, column, piece) takes 16 bytes of each lane.
+template <class E, class F>
+__device__ __forceinline__ void line_pieces(const f32x4_t (&a)[4], int lane, F&& f) {
+  const int row = lane & 7, second = (lane >> 3) & 1;
+  if constexpr (E::SZ == 2) {
+    float v[2][8];
+    pair_vals(a, 0, v[0]);
+    pair_vals(a, 1, v[1]);
+    u32x4_t x = E::Row::pack(v[0]), y = E::Row::pack(v[1]);
+    swap_rows(x, y);
+    f(row, pair_col(second, lane), x);
+    f(row + 8, pair_col(second, lane), y);
+  } else {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      u32x4_t x = __builtin_bit_cast(u32x4_t, a[2 * p]), y = __builtin_bit_cast(u32x4_t, a[2 * p + 1]);
+      swap_rows(x, y);
+      f(row, 32 * p + 16 * second + 4 * (lane >> 4), x);
+      f(row + 8, 32 * p + 16 * second + 4 * (lane >> 4), y);
+    }
+  }
+}
+
 // Division by the number of slots: p / k = (t + ((p - t) >> 1)) >> s with t = high word of
 // p m, m = floor(2^32 (2^(s + 1) - k) / k) + 1, 2^s < k <= 2^(s + 1), for any 32-bit p.
 struct PairDiv {
@@ -333,6 +378,14 @@ __device__ __forceinline__ void ring_loop(int stages, char* ring, int bytes, F& 
   mma(odd);
 }
 
+// 16 bytes to an offset of a buffer, nothing to kNowhere; the line leaves the caches
+// first.  That pays where all of its 128 bytes are written together: with half lines
+// the stores reach 2.5 TB/s and not 5.
+__device__ __forceinline__ void store_piece(const void* base, uint32_t off, u32x4_t v) {
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<void*>(base), 0, static_cast<int>(kBufBytes), 0x00020000);
+  __builtin_amdgcn_raw_buffer_store_b128(v, rs, static_cast<int>(off), 0, 2);
+}
 // 16-byte pieces of N elements to and from memory
 template <class E, int N>
 __device__ __forceinline__ void store_vals(typename E::T* p, const float (&v)[N]) {

@@ -10,8 +10,10 @@ struct DwArgs {
   const void *dg, *du, *h, *dy, *x;
   void *dgate, *dup, *ddown;
   const int32_t *offsets, *sorted_pair;
+  float* part;   // float32 partial sums [parts][3][E][I H] (parts > 1)
   PairDiv slots;
   int E, H, I, P;
+  int parts;   // of an expert's rows; 0: tiles of 256 x 256
   int strip;   // neighbouring tiles of a workgroup
   int unit;    // neighbouring strips on one XCD
 };

@@ -54,9 +54,37 @@ static RowCut best_cut(const moe_shape& s, int columns, int depth, bool half, bo
   return best;
 }
 
+// Parts of an expert's rows in the weight gradients, or 0 for tiles of 256 x 256.
+// Times in us for a stage of 64 bf16 (32 float32) rows, measured at 8192 rows, 2560 x
+// 5120: 128 x 128 tiles 0.7 alone to 1.5 for the two of a CU (float32 2 to 4), 256 x
+// 256, one per CU, 2.05 (float32 7).  One expert's 5000 rows of 2560 x 96 are 60
+// tiles of 79 stages: parts give the other CUs work.
+static int best_parts(const moe_shape& s) {
+  const bool f32 = s.act == MOE_DT_F32;
+  const auto up = [](double v, double d) { return static_cast<double>(static_cast<int64_t>((v + d - 1) / d)); };
+  const double mean = static_cast<double>(s.T) * s.top_k / s.E, stages = std::max(1.0, up(mean, f32 ? 32 : 64));
+  const double values = 3.0 * s.E * s.I * s.H;
+  const double tiles = 3 * s.E * up(s.I, 128) * up(s.H, 128), wide = 3 * s.E * up(s.I, 256) * up(s.H, 256);
+  int best = 1;
+  double least = 1e30;
+  for (int parts : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+    const double bytes = 4.0 * parts * values;
+    if (parts > 1 && (stages < 2 * parts || bytes > 128e6)) break;
+    const double n = tiles * parts, rounds = up(n, 512), both = std::min(1.0, n / 512);
+    const double us = rounds * (4 + (f32 ? 2 + 2 * both : 0.7 + 0.8 * both) * up(stages, parts)) +
+                      (parts > 1 ? 4 + 2 * bytes / 5e6 : 0);
+    if (us < least) {
+      least = us;
+      best = parts;
+    }
+  }
+  return stages > 2 && up(wide, 256) * (8 + (f32 ? 7 : 2.05) * stages) < least ? 0 : best;
+}
+
 void make_train_plan(const moe_shape& s, TrainPlan* p) {
   const size_t P = static_cast<size_t>(s.T) * s.top_k, a = act_bytes(s);
   *p = TrainPlan{};
+  p->dw_parts = best_parts(s);
   if (s.T == 0) return;
   p->gate_up = best_cut(s, s.I, s.H, true, true);
   // its loads and stores after the sum weigh more than what taller tiles save
@@ -81,6 +109,7 @@ void make_train_plan(const moe_shape& s, TrainPlan* p) {
     return c.parts > 1 ? static_cast<size_t>(c.parts) * P * columns * 4 : 0;
   };
   p->rows_part_off = take(std::max({part(p->gate_up, 2 * s.I), part(p->dh, s.I), part(p->dx, s.H)}));
+  p->dw_part_off = take(p->dw_parts > 1 ? static_cast<size_t>(p->dw_parts) * 3 * s.E * s.I * s.H * 4 : 0);
   const size_t products = at;
   at = 0;
   p->dl_off = take(P * 4);

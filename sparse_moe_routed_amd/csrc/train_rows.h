@@ -66,10 +66,10 @@ __device__ __forceinline__ bool tile_of_block(const RowArgs& a, int bm, int slab
 
 // Shapes of a workgroup: MW x NW waves, each 64 columns of MF fragments of rows,
 // STAGES in LDS.  PRODUCT: outputs of a matrix instruction, 16 x 16 or 32 x 32.
-template <int MW_, int NW_, int MF_, int STAGES_, int PRODUCT>
+template <int MW_, int NW_, int MF_, int STAGES_, int PRODUCT, bool ONCE_ = false>
 struct Shape {
   static constexpr int MW = MW_, NW = NW_, MF = MF_, STAGES = STAGES_;
-  static constexpr bool WIDE = PRODUCT == 32;
+  static constexpr bool WIDE = PRODUCT == 32, ONCE = ONCE_;
   static constexpr int NF = 64 / PRODUCT, KS = WIDE ? 4 : 2;       // fragments of columns, steps per stage
   static constexpr int WAVES = MW * NW, THREADS = 64 * WAVES;
   static constexpr int BM = PRODUCT * MF * MW, BN = 64 * NW;
@@ -78,6 +78,8 @@ struct Shape {
 };
 typedef Shape<2, 2, 1, 2, 16> Few;    // 32 x 128
 typedef Shape<2, 4, 4, 3, 16> Many;   // 128 x 256
+typedef Shape<2, 2, 1, 2, 16, true> FewOnce;
+typedef Shape<2, 4, 4, 3, 16, true> ManyOnce;
 typedef Shape<2, 4, 4, 2, 32> Wide;   // 256 x 256
 
 // What the tile products have in common: the waves' places, the layouts, the
@@ -118,7 +120,7 @@ struct Tiles {
     }
   }
   __device__ __forceinline__ void load_n(int j, u32x4_t rs, char* stage, uint32_t off) const {
-    load_lds(rs, stage + (j * S::WAVES + w) * 1024, off);
+    load_lds<S::ONCE>(rs, stage + (j * S::WAVES + w) * 1024, off);
   }
   __device__ __forceinline__ void load_m(int j, u32x4_t rs, char* stage, uint32_t off) const {
     load_lds(rs, stage + S::NBYTES + (j * S::WAVES + w) * 1024, off);
