@@ -252,6 +252,34 @@ def test_strips_of_many_experts(H, I, act):
         assert all(torch.equal(v, first[n]) for n, v in c.grads().items())
 
 
+# Sizes whose products are cut differently: tiles of 32, 128 and 256 rows, found by
+# the workgroups (up to 64 experts) or listed, sums whole or in parts, weights
+# read once or often; the last number of columns and rows inside a tile.
+CUTS = [
+    ("bf16", "act", 4096, 512, 1, 1056, 1), ("bf16", "8bit", 3000, 256, 70, 160, 10),
+    ("bf16", "8bit", 6000, 640, 2, 2080, 2), ("bf16", "act", 2500, 384, 2, 416, 1),
+    ("bf16", "8bit", 100, 2560, 8, 640, 8), ("bf16", "act", 900, 640, 70, 640, 8),
+    ("bf16", "8bit", 64, 2560, 1, 640, 1), ("bf16", "8bit", 140, 2560, 66, 32, 1),
+    ("bf16", "act", 4612, 2560, 1, 96, 1), ("f32", "act", 6000, 640, 2, 2080, 2),
+    ("f32", "8bit", 3000, 256, 70, 160, 10), ("f32", "8bit", 4100, 1280, 1, 2080, 1),
+    ("f32", "act", 2500, 384, 2, 416, 1), ("f32", "8bit", 130, 1280, 70, 320, 10),
+    ("f32", "act", 900, 640, 70, 640, 8), ("f32", "8bit", 200, 2560, 1, 96, 1)]
+
+
+@pytest.mark.parametrize("act,kept,T,H,E,I,k", CUTS)
+def test_every_cut(act, kept, T, H, E, I, k):
+    c = Case(T, H, E, I, k, act, kept, drop=0.1, seed=17)
+    c.save()
+    c.check_save(f"cut {T} {H} {E} {I} {k} {act} {kept}")
+    c = Case(T, H, E, I, k, act, kept, kept == "8bit", drop=0.1, seed=18)
+    c.fill_saved()
+    c.backward()
+    c.check_backward(f"cut {T} {H} {E} {I} {k} {act} {kept}")
+    first = {n: v.clone() for n, v in c.grads().items()}
+    c.backward()
+    assert all(torch.equal(v, first[n]) for n, v in c.grads().items())
+
+
 @pytest.mark.parametrize("kept", ["act", "8bit"])
 @pytest.mark.parametrize("T,E,k", [(50, 9, 2), (260, 2, 2)])
 def test_small_integers_are_exact(T, E, k, kept):
