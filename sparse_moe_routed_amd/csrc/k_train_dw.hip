@@ -318,16 +318,22 @@ __global__ __launch_bounds__(256) void k_join_dw(DwArgs a) {
 
 // Many rows per expert: one tile of 256 x 256 by eight waves, both sides through a
 // ring of two.
-template <class E>
+template <class E, bool JOIN>
 __global__ __launch_bounds__(512, 2) void k_dw_wide(DwArgs a) {
   typedef Wide S;
   constexpr int KR = E::SZ == 2 ? 4 : 2;          // k rows of a load
   constexpr int PAIRS_LDS = S::WAVES * 256;          // bytes of a stage's tokens, each wave its own
   __shared__ __align__(16) char lds[S::STAGES * S::BYTES + 4 * PAIRS_LDS];
   const int it = (a.I + S::BM - 1) / S::BM, ht = (a.H + S::BM - 1) / S::BM, blocks = it * ht;
-  const int total = 3 * blocks * a.E, per = (total + 7) / 8, turn = static_cast<int>(blockIdx.x >> 3);
-  const int item = static_cast<int>(blockIdx.x & 7) * per + turn;
-  if (turn >= per || item >= total) return;
+  const Tail tail(3 * blocks * a.E, a.mean_stages);
+  int item, part = 0, slot, cut = tail.cut;
+  if constexpr (JOIN) {
+    item = tail.full + blockIdx.x;
+    slot = blockIdx.x * cut;
+  } else {
+    if (!tail.item(blockIdx.x, item, part, slot)) return;
+    if (item < tail.full) cut = 1;
+  }
   const int e = item / (3 * blocks), in_e = item - e * 3 * blocks, which = in_e / blocks;
   const bool down = which == 2;
   const int mcols = down ? a.H : a.I, ncols = down ? a.I : a.H, ntiles = down ? it : ht;
@@ -357,15 +363,11 @@ __global__ __launch_bounds__(512, 2) void k_dw_wide(DwArgs a) {
     load_lds_word(rt, pair_lds + (s & 3) * PAIRS_LDS,
                   static_cast<uint32_t>(max(min(s * E::BK + pair_row, rows - 1), 0)) * 4);
   };
-  const int stages = (rows + E::BK - 1) / E::BK;
-  if (stages > 0) {
-    load_pairs(0);
-    load_pairs(1);
-    stage_barrier<0>();
-  }
-  T.run(
+  const int all = (rows + E::BK - 1) / E::BK, s0 = part * all / cut, stages = (part + 1) * all / cut - s0;
+  const auto products = [&] { T.run(
       stages, lds,
-      [&](int s, char* st) {
+      [&](int i, char* st) {
+        const int s = s0 + i;
         const int left = rows - s * E::BK;
         const int32_t* tok = reinterpret_cast<const int32_t*>(pair_lds + (s & 3) * PAIRS_LDS);
         const u32x4_t rm = buffer(mside + static_cast<size_t>(s) * E::BK * mcols * E::SZ);
@@ -388,7 +390,18 @@ __global__ __launch_bounds__(512, 2) void k_dw_wide(DwArgs a) {
 #pragma unroll
         for (int t = 0; t < S::MF; ++t)
           f.m[t] = frag32_cols<E, false>(st + S::NBYTES + T.wm * kBlockBytes, 32 * t, ks, lane);
-      });
+      }); };
+  if constexpr (JOIN) {
+    T.add_cuts(a.part, slot, cut);
+  } else {
+    if (stages > 0) {
+      load_pairs(s0);
+      load_pairs(s0 + 1);
+      stage_barrier<0>();
+    }
+    products();
+    if (cut > 1) return T.store_cut(a.part, slot);
+  }
 
   typename E::T* out = static_cast<typename E::T*>(down ? a.ddown : which ? a.dup : a.dgate) +
                        static_cast<size_t>(e) * a.I * a.H;
@@ -412,7 +425,13 @@ static hipError_t run(const moe_shape& s, DwArgs a, hipStream_t st) {
   const auto up = [](int v, int d) { return (v + d - 1) / d; };
   if (a.parts == 0) {
     const int total = 3 * s.E * up(s.I, Wide::BM) * up(s.H, Wide::BM);
-    k_dw_wide<E><<<up(total, 8) * 8, Wide::THREADS, 0, st>>>(a);
+    a.mean_stages = up(a.P / s.E, E::BK);
+    const Tail tail(total, a.mean_stages);
+    k_dw_wide<E, false><<<up(tail.full, 8) * 8 + up(tail.rest * tail.cut, 8) * 8, Wide::THREADS, 0, st>>>(a);
+    if (tail.cut > 1) {
+      if (const hipError_t e = hipGetLastError()) return e;
+      k_dw_wide<E, true><<<tail.rest, Wide::THREADS, 0, st>>>(a);
+    }
     return hipGetLastError();
   }
   const int it = up(s.I, 128), ht = s.H / 128;

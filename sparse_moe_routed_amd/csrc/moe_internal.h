@@ -201,6 +201,50 @@ struct RowCut {
 };
 constexpr int row_height(int shape) { return shape == kRowsFew ? 32 : shape == kRowsMany ? 128 : 256; }
 constexpr int kLookupExperts = 64;   // up to here a wave finds its tile itself
+#ifdef __HIPCC__
+#define MOE_BOTH __host__ __device__ inline
+#else
+#define MOE_BOTH inline
+#endif
+// Tiles of 256 x 256 take a CU each.  Those that are left when the others have filled
+// the 256 CUs `full / 256` times are cut along their sum, so that they fill them once
+// more, and another kernel joins them (8192 x 2560 x 5120: dx is 320 tiles, dw 600).
+constexpr int kCus = 256, kMostCuts = 4, kTailBytes = 256 * 256 * 4;
+struct Tail {
+  int full, rest, cut;
+  static constexpr bool possible(int stages) { return stages >= 16; }
+  MOE_BOTH Tail(int total, int stages) {
+    full = total / kCus * kCus;
+    rest = total - full;
+    cut = 1;
+    if (rest > 0 && rest <= kCus / 2) {
+      cut = kCus / rest;
+      if (cut > kMostCuts) cut = kMostCuts;
+      if (cut > stages / 8) cut = stages / 8;
+    }
+    if (cut < 2) {
+      full = total;
+      rest = 0;
+      cut = 1;
+    }
+  }
+  // Item of a workgroup: consecutive ones go to one XCD (workgroups are dealt to the
+  // 8 XCDs in turn).
+  MOE_BOTH bool item(int block, int& tile, int& part, int& slot) const {
+    int per = (full + 7) / 8, turn = block >> 3, at = (block & 7) * per + turn;
+    part = slot = 0;
+    tile = at;
+    if (turn < per) return at < full;
+    turn -= per;
+    per = (rest * cut + 7) / 8;
+    slot = (block & 7) * per + turn;
+    if (turn >= per || slot >= rest * cut) return false;
+    tile = full + slot / cut;
+    part = slot % cut;
+    return true;
+  }
+};
+
 // Workspace of one shape; the regions of the two products and of the router's
 // gradient overlap, as no call uses both.
 struct TrainPlan {
@@ -211,8 +255,8 @@ struct TrainPlan {
   size_t tiles_off[2];
   size_t x_off;         // act [T][H], x read back from an 8-bit checkpoint
   size_t dg_off, du_off, h_off;   // act [P][I]
-  size_t rows_part_off; // float [parts][P][columns]
-  size_t dw_part_off;   // float [dw_parts][3][E][I H]
+  size_t rows_part_off; // float [parts][P][columns], or the tiles of 256 x 256 that are cut
+  size_t dw_part_off;   // float [dw_parts][3][E][I H], or the same
   size_t dl_off;        // router: float [P]
   size_t total;
 };

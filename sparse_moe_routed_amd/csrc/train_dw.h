@@ -14,6 +14,7 @@ struct DwArgs {
   PairDiv slots;
   int E, H, I, P;
   int parts;   // of an expert's rows; 0: tiles of 256 x 256
+  int mean_stages;   // of an expert's rows (256 x 256)
   int strip;   // neighbouring tiles of a workgroup
   int unit;    // neighbouring strips on one XCD
 };

@@ -16,6 +16,13 @@ static double about_tiles(const moe_shape& s, int bm) {
   return s.E * std::max(1.0, static_cast<double>(static_cast<long long>((s.E > 1 ? 1.25 : 1.0) * mean + bm - 1) / bm));
 }
 
+// Rounds of 256 x 256 tiles over the CUs, and of those the time of the last ones' joining.
+static double wide_us(double tiles, int stages, double each) {
+  const Tail t(static_cast<int>(std::min(tiles, 1e9)), stages);
+  const double whole = static_cast<double>((t.full + kCus - 1) / kCus);
+  return whole * (8 + each * stages) + (t.cut > 1 ? 8 + each * stages / t.cut + 15 : 0);
+}
+
 // The cut with the least estimated time.  A product has `columns` columns and a
 // sum over `depth`; `half`: a tile has half as many columns (gate beside up).
 // Times in us for a stage of 64 bf16 (32 float32) of the sum, measured at 8192
@@ -43,8 +50,10 @@ static RowCut best_cut(const moe_shape& s, int columns, int depth, bool half, bo
       const double rounds = std::max(1.0, static_cast<double>(static_cast<long long>((n + slots - 1) / slots)));
       const double stage = shape == kRowsFew ? 0.6 + (f32 ? 1.4 : 1.1) * std::min(1.0, n / slots)
                            : shape == kRowsMany ? (f32 ? 3.6 : 1.2) : (f32 ? 6.9 : 1.95);
-      const double fixed = shape == kRowsFew ? 2 : shape == kRowsMany ? 4 : 8;
-      const double us = rounds * (fixed + stage * ((stages + parts - 1) / parts)) + (parts > 1 ? 4 + bytes / 5e6 : 0);
+      const double fixed = shape == kRowsFew ? 2 : 4;
+      const double us = shape == kRowsWide ? wide_us(n, stages, stage)
+                                           : rounds * (fixed + stage * ((stages + parts - 1) / parts)) +
+                                                 (parts > 1 ? 4 + bytes / 5e6 : 0);
       if (us < least) {
         least = us;
         best = RowCut{shape, parts};
@@ -78,7 +87,7 @@ static int best_parts(const moe_shape& s) {
       best = parts;
     }
   }
-  return stages > 2 && up(wide, 256) * (8 + (f32 ? 7 : 2.05) * stages) < least ? 0 : best;
+  return stages > 2 && wide_us(wide, static_cast<int>(stages), f32 ? 7 : 2.05) < least ? 0 : best;
 }
 
 void make_train_plan(const moe_shape& s, TrainPlan* p) {
@@ -108,8 +117,10 @@ void make_train_plan(const moe_shape& s, TrainPlan* p) {
   const auto part = [&](const RowCut& c, int columns) {
     return c.parts > 1 ? static_cast<size_t>(c.parts) * P * columns * 4 : 0;
   };
-  p->rows_part_off = take(std::max({part(p->gate_up, 2 * s.I), part(p->dh, s.I), part(p->dx, s.H)}));
-  p->dw_part_off = take(p->dw_parts > 1 ? static_cast<size_t>(p->dw_parts) * 3 * s.E * s.I * s.H * 4 : 0);
+  const auto tail = [](bool wide) { return wide ? static_cast<size_t>(kCus) * kTailBytes : 0; };
+  p->rows_part_off = take(std::max({part(p->gate_up, 2 * s.I), part(p->dh, s.I), part(p->dx, s.H),
+                                    tail(p->gate_up.shape == kRowsWide || p->dx.shape == kRowsWide)}));
+  p->dw_part_off = take(p->dw_parts > 1 ? static_cast<size_t>(p->dw_parts) * 3 * s.E * s.I * s.H * 4 : tail(p->dw_parts == 0));
   const size_t products = at;
   at = 0;
   p->dl_off = take(P * 4);

@@ -20,19 +20,22 @@ struct RowArgs {
   const int32_t *offsets, *sorted_pair;
   float* part;            // float [parts][P][columns] where the sum is split
   int most, E, H, I, P, parts;
+  bool cuts;              // 256 x 256: the last tiles are cut
   PairDiv slots;
 };
 
-// Tile, slab of columns and part of the sum of a workgroup.
+// Tile, slab of columns and part of the sum of a workgroup; `cut`: parts of this tile's
+// sum, `slot` its place among the parts.
 struct TileOf {
-  int e, row0, rows, slab, part;
+  int e, row0, rows, slab, part, cut, slot;
 };
 
-// Consecutive items go to one XCD (workgroups are dealt to the 8 XCDs in turn),
-// and run through bands of 8 tiles slab by slab: the tiles of a band share a
-// slab's weights where they are of one expert, and a tile's slabs share its
-// rows, in that XCD's L2.
-__device__ __forceinline__ bool tile_of_block(const RowArgs& a, int bm, int slabs, TileOf& o) {
+// Consecutive items run through bands of 8 tiles slab by slab: the tiles of a band
+// share a slab's weights where they are of one expert, and a tile's slabs share
+// its rows, in an XCD's L2.  `stages` of the whole sum; JOIN: the tiles that were cut.
+template <class S, bool JOIN>
+__device__ __forceinline__ bool tile_of_block(const RowArgs& a, int slabs, int stages, TileOf& o) {
+  constexpr int bm = S::BM;
   int n, row0 = 0, rows = 0, nt = 0, incl = 0;
   if (a.tiles) {
     n = __builtin_amdgcn_readfirstlane(a.tiles[3 * a.most]);
@@ -44,13 +47,24 @@ __device__ __forceinline__ bool tile_of_block(const RowArgs& a, int bm, int slab
     n = __builtin_amdgcn_readlane(incl, 63);
   }
   slabs *= a.parts;
-  const int total = n * slabs, per = (total + 7) / 8, s = static_cast<int>(blockIdx.x >> 3);
-  const int item = static_cast<int>(blockIdx.x & 7) * per + s;
-  if (s >= per || item >= total) return false;
+  const Tail tail(n * slabs, S::WIDE && a.cuts ? stages : 0);
+  int item, cut_part = 0;
+  o.cut = 1;
+  o.slot = 0;
+  if constexpr (JOIN) {
+    if (static_cast<int>(blockIdx.x) >= tail.rest) return false;
+    item = tail.full + blockIdx.x;
+    o.slot = blockIdx.x * tail.cut;
+    o.cut = tail.cut;
+  } else {
+    if (!tail.item(blockIdx.x, item, cut_part, o.slot)) return false;
+    if (item >= tail.full) o.cut = tail.cut;
+  }
   const int band = item / (8 * slabs), rest = item - band * 8 * slabs, wide = min(8, n - 8 * band);
   const int slab = rest / wide, t = 8 * band + rest - slab * wide;
   o.slab = slab / a.parts;
-  o.part = slab - o.slab * a.parts;
+  o.part = S::WIDE ? cut_part : slab - o.slab * a.parts;
+  if (!S::WIDE) o.cut = a.parts;
   if (a.tiles) {
     o.e = __builtin_amdgcn_readfirstlane(a.tiles[3 * t]);
     o.row0 = __builtin_amdgcn_readfirstlane(a.tiles[3 * t + 1]);
@@ -143,6 +157,33 @@ struct Tiles {
         else
           acc[t][i] = E::mma(f.n[i], f.m[t], acc[t][i]);
       }
+  }
+  // The sums of a part of a tile that is cut, as the lanes hold them, and all parts' sum.
+  __device__ __forceinline__ void store_cut(float* part, int slot) const {
+    f32x4_t* p = reinterpret_cast<f32x4_t*>(part + static_cast<size_t>(slot) * (kTailBytes / 4)) + threadIdx.x;
+#pragma unroll
+    for (int t = 0; t < S::MF; ++t)
+#pragma unroll
+      for (int i = 0; i < S::NF; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          p[((t * S::NF + i) * 4 + q) * S::THREADS] =
+              f32x4_t{acc[t][i][4 * q], acc[t][i][4 * q + 1], acc[t][i][4 * q + 2], acc[t][i][4 * q + 3]};
+  }
+  __device__ __forceinline__ void add_cuts(const float* part, int slot, int cuts) {
+    for (int c = 0; c < cuts; ++c) {
+      const f32x4_t* p = reinterpret_cast<const f32x4_t*>(part + static_cast<size_t>(slot + c) * (kTailBytes / 4)) + threadIdx.x;
+#pragma unroll
+      for (int t = 0; t < S::MF; ++t)
+#pragma unroll
+        for (int i = 0; i < S::NF; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4_t v = p[((t * S::NF + i) * 4 + q) * S::THREADS];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[t][i][4 * q + j] += v[j];
+          }
+    }
   }
   // M side in rows form
   __device__ __forceinline__ void read_m(const char* stage, int ks, Frags& f) const {
@@ -264,7 +305,7 @@ __device__ __forceinline__ uint32_t top_bits(const float (&v)[C]) {
 
 // One tile of BM rows x BN / 2 columns of g and of u.  N side: BN / 2 rows of W_gate
 // and the same of W_up, so both factors of h end in the same lane.
-template <class E, class S, int OUT>
+template <class E, class S, int OUT, bool JOIN = false>
 __global__ __launch_bounds__(S::THREADS, 2) void k_gate_up_save(RowArgs a, const void* __restrict__ x,
                                                                 const void* __restrict__ wg,
                                                                 const void* __restrict__ wu, GateUpOut o) {
@@ -272,7 +313,7 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_gate_up_save(RowArgs a, const
   constexpr int HALF = S::BN / 2, GL = S::NL / 2;
   const int H = a.H, I = a.I;
   TileOf tl;
-  if (!tile_of_block(a, S::BM, (I + HALF - 1) / HALF, tl)) return;
+  if (!tile_of_block<S, JOIN>(a, (I + HALF - 1) / HALF, H / E::BK, tl)) return;
   Tiles<E, S> T;
   const int col0 = tl.slab * HALF, lane = T.lane;
   const size_t wbase = (static_cast<size_t>(tl.e) * I + col0) * H * E::SZ;
@@ -292,9 +333,9 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_gate_up_save(RowArgs a, const
                            : kNowhere;
   }
 
-  const int stages = H / E::BK, s0 = OUT == kOutPart ? tl.part * stages / a.parts : 0;
-  T.run(
-      OUT == kOutPart ? (tl.part + 1) * stages / a.parts - s0 : stages, lds,
+  const int stages = H / E::BK, s0 = tl.part * stages / tl.cut;
+  const auto products = [&] { T.run(
+      (tl.part + 1) * stages / tl.cut - s0, lds,
       [&](int s, char* st) {
         const size_t k = static_cast<size_t>(s0 + s) * kStageBytes;
         const u32x4_t rg = buffer(gate + k), ru = buffer(up + k), rx = buffer(static_cast<const char*>(x) + k);
@@ -308,7 +349,14 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_gate_up_save(RowArgs a, const
       [&](const char* st, int ks, typename Tiles<E, S>::Frags& f) {
         T.read_gate_up(st, ks, f);
         T.read_m(st, ks, f);
-      });
+      }); };
+  if constexpr (JOIN) {
+    T.add_cuts(a.part, tl.slot, tl.cut);
+  } else {
+    products();
+    if constexpr (S::WIDE)
+      if (tl.cut > 1) return T.store_cut(a.part, tl.slot);
+  }
 
   constexpr int C = Tiles<E, S>::COLS;
   const int c = col0 + T.gate_col();
@@ -372,13 +420,13 @@ __device__ __forceinline__ void store_dh(const DhArgs& o, size_t at, const float
 }
 
 // dh of one tile of BM rows x BN columns.
-template <class E, class S, int OUT>
+template <class E, class S, int OUT, bool JOIN = false>
 __global__ __launch_bounds__(S::THREADS, 2) void k_dh(RowArgs a, const void* __restrict__ dy,
                                                       const void* __restrict__ wd, DhArgs o) {
   __shared__ __align__(16) char lds[S::STAGES * S::BYTES];
   const int H = a.H, I = a.I;
   TileOf tl;
-  if (!tile_of_block(a, S::BM, (I + S::BN - 1) / S::BN, tl)) return;
+  if (!tile_of_block<S, JOIN>(a, (I + S::BN - 1) / S::BN, H / E::BK, tl)) return;
   Tiles<E, S> T;
   const int col0 = tl.slab * S::BN;
   const char* down = static_cast<const char*>(wd) + (static_cast<size_t>(tl.e) * H * I + col0) * E::SZ;
@@ -389,9 +437,9 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_dh(RowArgs a, const void* __r
   T.rows_m(moff, tl.rows, [&](int r) { return static_cast<uint32_t>(r) * static_cast<uint32_t>(H * E::SZ); });
   T.cols(noff, krow, I * E::SZ, I - col0);
 
-  const int stages = H / E::BK, s0 = OUT == kOutPart ? tl.part * stages / a.parts : 0;
-  T.run(
-      OUT == kOutPart ? (tl.part + 1) * stages / a.parts - s0 : stages, lds,
+  const int stages = H / E::BK, s0 = tl.part * stages / tl.cut;
+  const auto products = [&] { T.run(
+      (tl.part + 1) * stages / tl.cut - s0, lds,
       [&](int s, char* st) {
         const u32x4_t rn = buffer(down + static_cast<size_t>(s0 + s) * E::BK * I * E::SZ);
         const u32x4_t rm = buffer(rows + static_cast<size_t>(s0 + s) * kStageBytes);
@@ -403,7 +451,14 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_dh(RowArgs a, const void* __r
       [&](const char* st, int ks, typename Tiles<E, S>::Frags& f) {
         T.read_n(st, ks, f);
         T.read_m(st, ks, f);
-      });
+      }); };
+  if constexpr (JOIN) {
+    T.add_cuts(a.part, tl.slot, tl.cut);
+  } else {
+    products();
+    if constexpr (S::WIDE)
+      if (tl.cut > 1) return T.store_cut(a.part, tl.slot);
+  }
 
 #pragma unroll
   for (int t = 0; t < S::MF; ++t) {
@@ -427,14 +482,14 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_dh(RowArgs a, const void* __r
 
 // drows of one tile of BM rows x BN columns: the stages run over I twice, dg with
 // W_gate, then du with W_up.
-template <class E, class S, int OUT>
+template <class E, class S, int OUT, bool JOIN = false>
 __global__ __launch_bounds__(S::THREADS, 2) void k_dx(RowArgs a, const void* __restrict__ dg,
                                                       const void* __restrict__ du, const void* __restrict__ wg,
                                                       const void* __restrict__ wu, void* __restrict__ drows) {
   __shared__ __align__(16) char lds[S::STAGES * S::BYTES];
   const int H = a.H, I = a.I;
   TileOf tl;
-  if (!tile_of_block(a, S::BM, (H + S::BN - 1) / S::BN, tl)) return;
+  if (!tile_of_block<S, JOIN>(a, (H + S::BN - 1) / S::BN, 2 * ((I + E::BK - 1) / E::BK), tl)) return;
   Tiles<E, S> T;
   const int col0 = tl.slab * S::BN, half = (I + E::BK - 1) / E::BK;
   const size_t wbase = (static_cast<size_t>(tl.e) * I * H + col0) * E::SZ;
@@ -447,9 +502,9 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_dx(RowArgs a, const void* __r
   // first k of this lane's chunk on the M side, the same for all its loads
   const int mchunk = ((T.lane & 7) ^ key_rows_m(rows_row(T.w, T.lane))) * (16 / E::SZ);
 
-  const int stages = 2 * half, s0 = OUT == kOutPart ? tl.part * stages / a.parts : 0;
-  T.run(
-      OUT == kOutPart ? (tl.part + 1) * stages / a.parts - s0 : stages, lds,
+  const int stages = 2 * half, s0 = tl.part * stages / tl.cut;
+  const auto products = [&] { T.run(
+      (tl.part + 1) * stages / tl.cut - s0, lds,
       [&](int i, char* st) {
         const int s = s0 + i, p = s >= half ? s - half : s, left = I - p * E::BK;   // k left from this stage on
         const char* wt = static_cast<const char*>(s >= half ? wu : wg) + wbase;
@@ -464,7 +519,14 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_dx(RowArgs a, const void* __r
       [&](const char* st, int ks, typename Tiles<E, S>::Frags& f) {
         T.read_n(st, ks, f);
         T.read_m(st, ks, f);
-      });
+      }); };
+  if constexpr (JOIN) {
+    T.add_cuts(a.part, tl.slot, tl.cut);
+  } else {
+    products();
+    if constexpr (S::WIDE)
+      if (tl.cut > 1) return T.store_cut(a.part, tl.slot);
+  }
 
 #pragma unroll
   for (int t = 0; t < S::MF; ++t) {
@@ -559,17 +621,25 @@ inline T* at_off(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
-inline int tile_grid(const RowArgs& a, int bm, int slabs) {
-  const int tiles = a.P / bm + (a.E < a.P ? a.E : a.P);
-  return (tiles * slabs * a.parts + 7) / 8 * 8;
+template <class S>
+int tile_grid(const RowArgs& a, int slabs) {
+  const int tiles = a.P / S::BM + (a.E < a.P ? a.E : a.P);
+  return (tiles * slabs * a.parts + 7) / 8 * 8 + (S::WIDE ? kCus : 0);
+}
+// Whether the last tiles are cut: the tiles of one expert are known here.
+template <class S>
+bool cuts_tail(const RowArgs& a, int slabs, int stages) {
+  if (!S::WIDE || !Tail::possible(stages)) return false;
+  return a.E > 1 || Tail((a.P + S::BM - 1) / S::BM * slabs, stages).cut > 1;
 }
 inline int join_grid(const RowArgs& a, int columns) {
   return static_cast<int>((static_cast<size_t>(a.P) * columns / 8 + 255) / 256);
 }
 
 template <class E, class S>
-hipError_t run_gate_up(const RowArgs& a, const void* x, const moe_experts& ex, const GateUpOut& o, hipStream_t st) {
-  const int grid = tile_grid(a, S::BM, (2 * a.I + S::BN - 1) / S::BN);
+hipError_t run_gate_up(RowArgs a, const void* x, const moe_experts& ex, const GateUpOut& o, hipStream_t st) {
+  const int slabs = (2 * a.I + S::BN - 1) / S::BN, grid = tile_grid<S>(a, slabs);
+  a.cuts = cuts_tail<S>(a, slabs, a.H / E::BK);
   const bool q8 = o.g_scale != nullptr;
   if constexpr (!S::WIDE) {
     if (a.parts > 1) {
@@ -582,12 +652,18 @@ hipError_t run_gate_up(const RowArgs& a, const void* x, const moe_experts& ex, c
   }
   const auto kernel = q8 ? k_gate_up_save<E, S, kOut8> : k_gate_up_save<E, S, kOutAct>;
   kernel<<<grid, S::THREADS, 0, st>>>(a, x, ex.gate, ex.up, o);
+  if constexpr (S::WIDE)
+    if (a.cuts) {
+      if (const hipError_t e = hipGetLastError()) return e;
+      const auto join = q8 ? k_gate_up_save<E, S, kOut8, true> : k_gate_up_save<E, S, kOutAct, true>;
+      join<<<kCus / 2, S::THREADS, 0, st>>>(a, x, ex.gate, ex.up, o);
+    }
   return hipGetLastError();
 }
 
 template <class E, class S>
 hipError_t run_dh(const RowArgs& a, const void* dy, const void* down, const DhArgs& o, hipStream_t st) {
-  const int grid = tile_grid(a, S::BM, (a.I + S::BN - 1) / S::BN);
+  const int grid = tile_grid<S>(a, (a.I + S::BN - 1) / S::BN);
   const bool q8 = o.g_scale != nullptr;
   if (a.parts > 1) {
     k_dh<E, S, kOutPart><<<grid, S::THREADS, 0, st>>>(a, dy, down, o);
@@ -602,8 +678,9 @@ hipError_t run_dh(const RowArgs& a, const void* dy, const void* down, const DhAr
 }
 
 template <class E, class S>
-hipError_t run_dx(const RowArgs& a, const DhArgs& d, const moe_experts& ex, void* drows, hipStream_t st) {
-  const int grid = tile_grid(a, S::BM, (a.H + S::BN - 1) / S::BN);
+hipError_t run_dx(RowArgs a, const DhArgs& d, const moe_experts& ex, void* drows, hipStream_t st) {
+  const int slabs = (a.H + S::BN - 1) / S::BN, grid = tile_grid<S>(a, slabs);
+  a.cuts = cuts_tail<S>(a, slabs, 2 * ((a.I + E::BK - 1) / E::BK));
   if constexpr (!S::WIDE) {
     if (a.parts > 1) {
       k_dx<E, S, kOutPart><<<grid, S::THREADS, 0, st>>>(a, d.dg, d.du, ex.gate, ex.up, drows);
@@ -613,6 +690,11 @@ hipError_t run_dx(const RowArgs& a, const DhArgs& d, const moe_experts& ex, void
     }
   }
   k_dx<E, S, kOutAct><<<grid, S::THREADS, 0, st>>>(a, d.dg, d.du, ex.gate, ex.up, drows);
+  if constexpr (S::WIDE)
+    if (a.cuts) {
+      if (const hipError_t e = hipGetLastError()) return e;
+      k_dx<E, S, kOutAct, true><<<kCus / 2, S::THREADS, 0, st>>>(a, d.dg, d.du, ex.gate, ex.up, drows);
+    }
   return hipGetLastError();
 }
 

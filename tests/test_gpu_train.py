@@ -263,7 +263,11 @@ CUTS = [
     ("bf16", "act", 4612, 2560, 1, 96, 1), ("f32", "act", 6000, 640, 2, 2080, 2),
     ("f32", "8bit", 3000, 256, 70, 160, 10), ("f32", "8bit", 4100, 1280, 1, 2080, 1),
     ("f32", "act", 2500, 384, 2, 416, 1), ("f32", "8bit", 130, 1280, 70, 320, 10),
-    ("f32", "act", 900, 640, 70, 640, 8), ("f32", "8bit", 200, 2560, 1, 96, 1)]
+    ("f32", "act", 900, 640, 70, 640, 8), ("f32", "8bit", 200, 2560, 1, 96, 1),
+    # the last tiles' sums cut
+    ("bf16", "act", 7000, 768, 1, 1600, 1), ("bf16", "8bit", 8000, 1152, 1, 1280, 1),
+    ("bf16", "8bit", 6500, 1280, 1, 2592, 1), ("bf16", "act", 6100, 1280, 5, 1056, 2),
+    ("f32", "act", 7000, 768, 1, 1600, 1), ("f32", "8bit", 8000, 1024, 1, 1056, 1)]
 
 
 @pytest.mark.parametrize("act,kept,T,H,E,I,k", CUTS)
