@@ -9,32 +9,44 @@
 
 namespace moe {
 
-// One workgroup per token: dl of its pairs, then dx.
-template <class A>
-__global__ __launch_bounds__(256) void k_router_dx(RouterBwd a, int H, int E, int k) {
+// w . dw of a token's slots, and dl of one of them
+__device__ __forceinline__ float slots_dot(const RouterBwd& a, size_t p0, int k) {
+  float dot = 0.f;
+  for (int j = 0; j < k; ++j) dot = fmaf(a.w[p0 + j], a.dw[p0 + j], dot);
+  return dot;
+}
+
+// One workgroup per token: dl of its pairs, then dx.  JOINT: every thread takes the
+// dot product itself, and dl is not kept.
+template <class A, bool JOINT>
+__device__ __forceinline__ void dx_token(const RouterBwd& a, int H, int E, int k, int block) {
   typedef typename A::T T;
   constexpr int V = A::VEC, DEEP = 4;
   __shared__ float dl[1024];
   __shared__ int expert[1024];
   __shared__ float part[4];
-  const size_t p0 = static_cast<size_t>(blockIdx.x) * k;
+  const size_t p0 = static_cast<size_t>(block) * k;
   float dot = 0.f;
-  for (int j = threadIdx.x; j < k; j += 256) dot = fmaf(a.w[p0 + j], a.dw[p0 + j], dot);
-  dot = wave_sum_f32(dot);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
-  __syncthreads();
-  dot = (part[0] + part[1]) + (part[2] + part[3]);
+  if constexpr (JOINT) {
+    dot = slots_dot(a, p0, k);
+  } else {
+    for (int j = threadIdx.x; j < k; j += 256) dot = fmaf(a.w[p0 + j], a.dw[p0 + j], dot);
+    dot = wave_sum_f32(dot);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+    __syncthreads();
+    dot = (part[0] + part[1]) + (part[2] + part[3]);
+  }
   for (int j = threadIdx.x; j < k; j += 256) {
     const float d = a.w[p0 + j] * (a.dw[p0 + j] - dot);
     const int e = a.ids[p0 + j];
     dl[j] = d;
     expert[j] = static_cast<uint32_t>(e) < static_cast<uint32_t>(E) ? e : -1;   // -1: a dropped pair
-    a.dl[p0 + j] = d;
+    if constexpr (!JOINT) a.dl[p0 + j] = d;
   }
   __syncthreads();
   if (!a.dx) return;
   const T* wr = static_cast<const T*>(a.w_router);
-  const size_t row = static_cast<size_t>(blockIdx.x) * H;
+  const size_t row = static_cast<size_t>(block) * H;
   for (int h = threadIdx.x * V; h < H; h += 256 * V) {
     float v[V];
     if (a.dx_in)
@@ -60,6 +72,10 @@ __global__ __launch_bounds__(256) void k_router_dx(RouterBwd a, int H, int E, in
     *reinterpret_cast<u32x4_t*>(static_cast<T*>(a.dx) + row + h) = A::pack(v);
   }
 }
+template <class A>
+__global__ __launch_bounds__(256) void k_router_dx(RouterBwd a, int H, int E, int k) {
+  dx_token<A, false>(a, H, E, k, blockIdx.x);
+}
 
 // One workgroup per expert and LANES 16-byte columns; its lane groups share the
 // rows.  Tokens and gradients of 64 WAVES rows are read at once, into LDS, and
@@ -68,16 +84,16 @@ __global__ __launch_bounds__(256) void k_router_dx(RouterBwd a, int H, int E, in
 // tokens, 10 of 512 experts, H 2560, bf16 gather 210 MB in 29.8 us; columns of
 // 1024 bytes take 44.8 and eight waves of 256 bytes 44.5.  Without the rows of
 // eight loads together it was 112.
-template <class A, int WAVES, int LANES>
-__global__ __launch_bounds__(64 * WAVES) void k_router_dw(RouterBwd a, int H, int P, PairDiv slots) {
+template <class A, int WAVES, int LANES, bool JOINT>
+__device__ __forceinline__ void dw_columns(const RouterBwd& a, int H, int P, PairDiv slots, int e, int column) {
   typedef typename A::T T;
   constexpr int V = A::VEC, THREADS = 64 * WAVES, GROUPS = THREADS / LANES, DEEP = 8;
   __shared__ uint32_t token[THREADS];
   __shared__ float grad[THREADS];
   __shared__ float sums[GROUPS][LANES * V + 4];
   __shared__ float bias[WAVES];
-  const int e = blockIdx.x, tid = threadIdx.x, g = tid / LANES;
-  const int h = (blockIdx.y * LANES + tid % LANES) * V;
+  const int tid = threadIdx.x, g = tid / LANES;
+  const int h = (column * LANES + tid % LANES) * V;
   const bool cols = a.dw_router && h < H;
   int row0 = 0, rows = 0;
   if (P > 0) {
@@ -90,8 +106,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_router_dw(RouterBwd a, int H, in
     const int here = min(rows - r0, THREADS);
     if (tid < here) {
       const int p = min(max(a.sorted_pair[row0 + r0 + tid], 0), P - 1);
-      const float d = a.dl[p];
-      token[tid] = slots.div(p);
+      const uint32_t t = slots.div(p);
+      float d;
+      if constexpr (JOINT)
+        d = a.w[p] * (a.dw[p] - slots_dot(a, static_cast<size_t>(t) * slots.k, slots.k));
+      else
+        d = a.dl[p];
+      token[tid] = t;
       grad[tid] = d;
       db += d;
     }
@@ -122,18 +143,32 @@ __global__ __launch_bounds__(64 * WAVES) void k_router_dw(RouterBwd a, int H, in
   __syncthreads();
   if (a.dw_router)
     for (int i = tid; i < LANES * V; i += THREADS) {
-      const int c = blockIdx.y * LANES * V + i;
+      const int c = column * LANES * V + i;
       float sum = sums[0][i];
 #pragma unroll
       for (int j = 1; j < GROUPS; ++j) sum += sums[j][i];
       if (c < H) a.dw_router[static_cast<size_t>(e) * H + c] = sum;
     }
-  if (a.dbias && blockIdx.y == 0 && tid == 0) {
+  if (a.dbias && column == 0 && tid == 0) {
     db = bias[0];
 #pragma unroll
     for (int j = 1; j < WAVES; ++j) db += bias[j];
     a.dbias[e] = db;
   }
+}
+template <class A, int WAVES, int LANES>
+__global__ __launch_bounds__(64 * WAVES) void k_router_dw(RouterBwd a, int H, int P, PairDiv slots) {
+  dw_columns<A, WAVES, LANES, false>(a, H, P, slots, blockIdx.x, blockIdx.y);
+}
+
+// Both in one launch, with the experts' workgroups first.
+template <class A, int LANES>
+__global__ __launch_bounds__(256) void k_router(RouterBwd a, int H, int E, int P, PairDiv slots, int columns) {
+  const int block = blockIdx.x;
+  if (block < E * columns)
+    dw_columns<A, 4, LANES, true>(a, H, P, slots, block % E, block / E);
+  else
+    dx_token<A, true>(a, H, E, slots.k, block - E * columns);
 }
 
 template <class A, int WAVES, int LANES>
@@ -144,15 +179,30 @@ static hipError_t run_dw(const moe_shape& s, const RouterBwd& a, hipStream_t st)
   return hipGetLastError();
 }
 
+template <class A, int LANES>
+static hipError_t run_joint(const moe_shape& s, const RouterBwd& a, hipStream_t st) {
+  const int columns = a.dw_router ? (s.H + LANES * A::VEC - 1) / (LANES * A::VEC) : 1;
+  k_router<A, LANES><<<s.E * columns + (a.dx ? s.T : 0), 256, 0, st>>>(a, s.H, s.E, s.T * s.top_k,
+                                                                      PairDiv::of(s.top_k), columns);
+  return hipGetLastError();
+}
+
 template <class A>
 static hipError_t run(const moe_shape& s, const RouterBwd& a, hipStream_t st) {
+  // Few workgroups: narrower columns and more waves for the experts' many rows.
+  const bool few = static_cast<long long>(s.E) * s.H < 512 * 32 * A::VEC;
+  // A small call is its launches (333 tokens top-3 of 60, 384 float32: 8.4 -> 4.8 us;
+  // 1500 top-4 of 128, 1280 float32, 31 MB of gathered rows: 13.1 -> 9.9); at 41 MB the
+  // dot products taken again cost as much, at 210 MB a third more.
+  const long long P = static_cast<long long>(s.T) * s.top_k;
+  if (P > 0 && s.top_k <= 16 && (a.dw_router || a.dbias) && P <= 512ll * s.E &&
+      P * s.H * static_cast<int>(sizeof(typename A::T)) <= 32 << 20)
+    return few ? run_joint<A, 16>(s, a, st) : run_joint<A, 32>(s, a, st);
   if (s.T > 0) {
     k_router_dx<A><<<s.T, 256, 0, st>>>(a, s.H, s.E, s.top_k);
     if (const hipError_t e = hipGetLastError()) return e;
   }
   if (!a.dw_router && !a.dbias) return hipSuccess;
-  // Few workgroups: narrower columns and more waves for the experts' many rows.
-  const bool few = static_cast<long long>(s.E) * s.H < 512 * 32 * A::VEC;
   return few ? run_dw<A, 16, 16>(s, a, st) : run_dw<A, 4, 32>(s, a, st);
 }
 

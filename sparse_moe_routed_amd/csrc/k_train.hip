@@ -106,6 +106,9 @@ hipError_t launch_gate_up_save(const moe_shape& s, const TrainPlan& pl, const vo
                               : gate_up<TF32>(s, pl, x, ex, pm, sv, h, ws, st);
 }
 
+// Most workgroups of the rows' gradient that share the weight gradients' launch.
+constexpr int kJointBlocks = 512;
+
 template <class E>
 static hipError_t rows_backward(const moe_shape& s, const TrainPlan& pl, const void* dy, const DhArgs& d,
                                 const moe_experts& ex, const moe_perm& pm, void* drows, void* ws, hipStream_t st) {
@@ -123,6 +126,8 @@ hipError_t launch_ffn_backward(const moe_shape& s, const TrainPlan& plan, const 
   TrainPlan pl = plan;
   const bool bf16 = s.act == MOE_DT_BF16;
   DwArgs a{};
+  DxArgs dx{};
+  bool joint = false;
   a.E = s.E;
   a.H = s.H;
   a.I = s.I;
@@ -140,6 +145,16 @@ hipError_t launch_ffn_backward(const moe_shape& s, const TrainPlan& plan, const 
     }
     const DhArgs d{sv->g, sv->u, sv->g_scale, sv->u_scale, at_off<char>(ws, pl.dg_off), at_off<char>(ws, pl.du_off),
                    at_off<char>(ws, pl.h_off)};
+    joint = drows && dex && pl.dx.shape == kRowsFew && pl.dx.parts == 1 && pl.dw_parts == 1;
+    if (joint) {
+      dx.rows = row_args(s, pl, *pm, ws, pl.dx);
+      dx.gate = ex.gate;
+      dx.up = ex.up;
+      dx.drows = drows;
+      dx.blocks = tile_grid<Few>(dx.rows, s.H / 128);
+      joint = dx.blocks <= kJointBlocks;
+    }
+    if (joint) drows = nullptr;
     if (e == hipSuccess)
       e = bf16 ? rows_backward<TBf16>(s, pl, dy, d, ex, *pm, drows, ws, st)
                : rows_backward<TF32>(s, pl, dy, d, ex, *pm, drows, ws, st);
@@ -159,7 +174,7 @@ hipError_t launch_ffn_backward(const moe_shape& s, const TrainPlan& plan, const 
   a.dgate = const_cast<void*>(dex->gate);
   a.dup = const_cast<void*>(dex->up);
   a.ddown = const_cast<void*>(dex->down);
-  return launch_dw(s, a, st);
+  return launch_dw(s, a, joint ? &dx : nullptr, st);
 }
 
 }  // namespace moe

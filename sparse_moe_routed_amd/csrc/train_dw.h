@@ -19,6 +19,14 @@ struct DwArgs {
   int unit;    // neighbouring strips on one XCD
 };
 
-hipError_t launch_dw(const moe_shape& s, const DwArgs& a, hipStream_t st);
+// The rows' gradient by the same launch, tiles of 32 rows (parts 1 only).
+struct DxArgs {
+  RowArgs rows;
+  const void *gate, *up;
+  void* drows;
+  int blocks;   // workgroups, a multiple of 8
+};
+
+hipError_t launch_dw(const moe_shape& s, const DwArgs& a, const DxArgs* x, hipStream_t st);
 
 }  // namespace moe

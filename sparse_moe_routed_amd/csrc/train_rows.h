@@ -34,7 +34,7 @@ struct TileOf {
 // share a slab's weights where they are of one expert, and a tile's slabs share
 // its rows, in an XCD's L2.  `stages` of the whole sum; JOIN: the tiles that were cut.
 template <class S, bool JOIN>
-__device__ __forceinline__ bool tile_of_block(const RowArgs& a, int slabs, int stages, TileOf& o) {
+__device__ __forceinline__ bool tile_of_block(const RowArgs& a, int slabs, int stages, int block, TileOf& o) {
   constexpr int bm = S::BM;
   int n, row0 = 0, rows = 0, nt = 0, incl = 0;
   if (a.tiles) {
@@ -52,12 +52,12 @@ __device__ __forceinline__ bool tile_of_block(const RowArgs& a, int slabs, int s
   o.cut = 1;
   o.slot = 0;
   if constexpr (JOIN) {
-    if (static_cast<int>(blockIdx.x) >= tail.rest) return false;
-    item = tail.full + blockIdx.x;
-    o.slot = blockIdx.x * tail.cut;
+    if (block >= tail.rest) return false;
+    item = tail.full + block;
+    o.slot = block * tail.cut;
     o.cut = tail.cut;
   } else {
-    if (!tail.item(blockIdx.x, item, cut_part, o.slot)) return false;
+    if (!tail.item(block, item, cut_part, o.slot)) return false;
     if (item >= tail.full) o.cut = tail.cut;
   }
   const int band = item / (8 * slabs), rest = item - band * 8 * slabs, wide = min(8, n - 8 * band);
@@ -313,7 +313,7 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_gate_up_save(RowArgs a, const
   constexpr int HALF = S::BN / 2, GL = S::NL / 2;
   const int H = a.H, I = a.I;
   TileOf tl;
-  if (!tile_of_block<S, JOIN>(a, (I + HALF - 1) / HALF, H / E::BK, tl)) return;
+  if (!tile_of_block<S, JOIN>(a, (I + HALF - 1) / HALF, H / E::BK, blockIdx.x, tl)) return;
   Tiles<E, S> T;
   const int col0 = tl.slab * HALF, lane = T.lane;
   const size_t wbase = (static_cast<size_t>(tl.e) * I + col0) * H * E::SZ;
@@ -426,7 +426,7 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_dh(RowArgs a, const void* __r
   __shared__ __align__(16) char lds[S::STAGES * S::BYTES];
   const int H = a.H, I = a.I;
   TileOf tl;
-  if (!tile_of_block<S, JOIN>(a, (I + S::BN - 1) / S::BN, H / E::BK, tl)) return;
+  if (!tile_of_block<S, JOIN>(a, (I + S::BN - 1) / S::BN, H / E::BK, blockIdx.x, tl)) return;
   Tiles<E, S> T;
   const int col0 = tl.slab * S::BN;
   const char* down = static_cast<const char*>(wd) + (static_cast<size_t>(tl.e) * H * I + col0) * E::SZ;
@@ -482,14 +482,13 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_dh(RowArgs a, const void* __r
 
 // drows of one tile of BM rows x BN columns: the stages run over I twice, dg with
 // W_gate, then du with W_up.
-template <class E, class S, int OUT, bool JOIN = false>
-__global__ __launch_bounds__(S::THREADS, 2) void k_dx(RowArgs a, const void* __restrict__ dg,
-                                                      const void* __restrict__ du, const void* __restrict__ wg,
-                                                      const void* __restrict__ wu, void* __restrict__ drows) {
-  __shared__ __align__(16) char lds[S::STAGES * S::BYTES];
+template <class E, class S, int OUT, bool JOIN>
+__device__ __forceinline__ void dx_tile(const RowArgs& a, const void* __restrict__ dg, const void* __restrict__ du,
+                                        const void* __restrict__ wg, const void* __restrict__ wu,
+                                        void* __restrict__ drows, char* lds, int block) {
   const int H = a.H, I = a.I;
   TileOf tl;
-  if (!tile_of_block<S, JOIN>(a, (H + S::BN - 1) / S::BN, 2 * ((I + E::BK - 1) / E::BK), tl)) return;
+  if (!tile_of_block<S, JOIN>(a, (H + S::BN - 1) / S::BN, 2 * ((I + E::BK - 1) / E::BK), block, tl)) return;
   Tiles<E, S> T;
   const int col0 = tl.slab * S::BN, half = (I + E::BK - 1) / E::BK;
   const size_t wbase = (static_cast<size_t>(tl.e) * I * H + col0) * E::SZ;
@@ -544,6 +543,13 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_dx(RowArgs a, const void* __r
         store_vals<E>(static_cast<typename E::T*>(drows) + row * H + c, v);
     }
   }
+}
+template <class E, class S, int OUT, bool JOIN = false>
+__global__ __launch_bounds__(S::THREADS, 2) void k_dx(RowArgs a, const void* __restrict__ dg,
+                                                      const void* __restrict__ du, const void* __restrict__ wg,
+                                                      const void* __restrict__ wu, void* __restrict__ drows) {
+  __shared__ __align__(16) char lds[S::STAGES * S::BYTES];
+  dx_tile<E, S, OUT, JOIN>(a, dg, du, wg, wu, drows, lds, blockIdx.x);
 }
 
 // ---- joining the parts of the sums: 8 columns a thread, parts in order ----
