@@ -2,14 +2,14 @@
 // LDS and multiplied on the matrix cores, for bf16 and float32 alike.
 //
 // A product D[m][n] = sum_k M(m, k) N(n, k) is computed in tiles, each wave 64
-// columns (n) of 64 or 16 rows (m).  Many rows: 128 x 256 outputs by eight waves
-// (2 x 4), three stages in LDS (144 KB, one workgroup per CU).  Few rows: 32 x
-// 128 by four waves (2 x 2), two stages (40 KB, four workgroups).  A stage holds
-// 128 bytes of k per row: 64 bf16 or 32 float32.  The N side is MFMA's first
-// operand and the M side its second, so a lane of the result (i = lane % 16, q =
-// lane / 16) holds columns 4 q .. 4 q + 3 of a fragment's 16 and row i: after one
-// exchange between lanes it stores 8 neighbouring columns (16 bytes of bf16)
-// of its row itself.
+// columns (n) of 16, 64 or 128 rows (m).  Few rows: 32 x 128 outputs by four waves (2
+// x 2), two stages in LDS (40 KB, four workgroups per CU).  Many rows: 128 x 256 by
+// eight waves (2 x 4), three stages (144 KB, one workgroup).  Wide: 256 x 256 by eight
+// waves, 32 x 32 matrix instructions, two stages (128 KB).  A stage holds 128 bytes
+// of k per row: 64 bf16 or 32 float32.  The N side is MFMA's first operand and the M
+// side its second, so a lane of a 16 x 16 result (i = lane % 16, q = lane / 16) holds
+// columns 4 q .. 4 q + 3 of a fragment's 16 and row i: after one exchange between
+// lanes it stores 8 neighbouring columns (16 bytes of bf16) of its row itself.
 //
 // Either side comes in one of two forms:
 //   rows:    k is contiguous in memory.  LDS holds [row][128 bytes of k].
@@ -396,20 +396,6 @@ __device__ __forceinline__ void store_vals(typename E::T* p, const float (&v)[N]
 #pragma unroll
     for (int e = 0; e < V; ++e) t[e] = v[c * V + e];
     *reinterpret_cast<u32x4_t*>(p + c * V) = E::Row::pack(t);
-  }
-}
-// ... to an offset of a buffer: the same number of stores whatever `off` is
-template <class E, int N>
-__device__ __forceinline__ void store_vals(const void* base, uint32_t off, const float (&v)[N]) {
-  constexpr int V = E::Row::VEC;
-  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<void*>(base), 0, static_cast<int>(kBufBytes), 0x00020000);
-#pragma unroll
-  for (int c = 0; c < N / V; ++c) {
-    float t[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) t[e] = v[c * V + e];
-    __builtin_amdgcn_raw_buffer_store_b128(E::Row::pack(t), rs, static_cast<int>(off + 16 * c), 0, 0);
   }
 }
 template <class E, int N>
