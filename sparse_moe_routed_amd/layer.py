@@ -156,28 +156,35 @@ class MoELayerBuffers:
         return _abi.moe_route_backward(self.shape, self.topk_ids, self.topk_w, dw, dlogits, stream)
 
     def _train(self, kept=None):
-        """Memory for training, once: the workspace, gradients of the rows and
-        route weights, and g and u ('act', or '8bit' with their scales)."""
-        dev, dt, P = self.topk_ids.device, self.y.dtype, self.T * self.k
+        """Memory for training, made once and kept as long as the buffer (work
+        that is queued or captured in a graph may hold its addresses): the
+        workspace, and a set of g and u for each form that was asked for ('act',
+        or '8bit' with their scales).  Attributes change only once all memory
+        of a set is there."""
+        dev = self.topk_ids.device
         if not hasattr(self, "train_ws"):
-            self.train_ws_bytes = _abi.moe_train_workspace_size(self.shape)
-            self.train_ws = torch.empty(max(self.train_ws_bytes, 1), dtype=torch.uint8, device=dev)
-        if kept is not None and kept != getattr(self, "kept", None):
-            if kept not in ("act", "8bit"):
-                raise ValueError(f"kept must be 'act' or '8bit', not {kept!r}")
-            self.g_scale = self.u_scale = None
-            if kept == "8bit":
-                dt = torch.int8
-                self.g_scale = torch.empty((P, self.I // 32), dtype=torch.uint8, device=dev)
-                self.u_scale = torch.empty((P, self.I // 32), dtype=torch.uint8, device=dev)
-            self.g = torch.empty((P, self.I), dtype=dt, device=dev)
-            self.u = torch.empty((P, self.I), dtype=dt, device=dev)
-            self.saved = _abi.make_saved(self.g, self.u, self.g_scale, self.u_scale)
-            self.kept = kept
+            n = _abi.moe_train_workspace_size(self.shape)
+            self.train_ws, self.train_ws_bytes = torch.empty(max(n, 1), dtype=torch.uint8, device=dev), n
+            self._kept_sets = {}
+        if kept is None:
+            return
+        if kept not in ("act", "8bit"):
+            raise ValueError(f"kept must be 'act' or '8bit', not {kept!r}")
+        if kept not in self._kept_sets:
+            P, q8 = self.T * self.k, kept == "8bit"
+            dt = torch.int8 if q8 else self.y.dtype
+            g, u = (torch.empty((P, self.I), dtype=dt, device=dev) for _ in range(2))
+            gs, us = (torch.empty((P, self.I // 32), dtype=torch.uint8, device=dev) if q8 else None
+                      for _ in range(2))
+            self._kept_sets[kept] = (g, u, gs, us, _abi.make_saved(g, u, gs, us))
+        self.kept = kept
+        self.g, self.u, self.g_scale, self.u_scale, self.saved = self._kept_sets[kept]
 
     def ffn_gate_up_save(self, x, experts, kept="act", perm=None, h=None, stream=None):
         """moe_ffn_gate_up_save into this buffer's h and saved (g and u, kept in
-        the activation type or in 8 bits)."""
+        the activation type or in 8 bits).  Each form has memory of its own,
+        which stays; ffn_backward reads that of the last call of this method
+        (the replay of a graph is none)."""
         self._train(kept)
         return _abi.moe_ffn_gate_up_save(self.shape, x, experts, self.perm if perm is None else perm,
                                          self.saved, self.h if h is None else h, self.train_ws,
@@ -220,8 +227,8 @@ class MoELayerBuffers:
         (x_scale)."""
         self._train()
         if not hasattr(self, "dy"):
-            self.dy, self.drows = torch.empty_like(self.y), torch.empty_like(self.y)
-            self.dw, self.dx_rows = torch.empty_like(self.topk_w), torch.empty_like(self.out)
+            made = [torch.empty_like(t) for t in (self.y, self.y, self.topk_w, self.out)]
+            self.dy, self.drows, self.dw, self.dx_rows = made
         if x_scale is not None:
             if not hasattr(self, "x_back"):
                 self.x_back = torch.empty_like(self.out)
