@@ -2,9 +2,22 @@
 of the layer runs in libmoe.so)."""
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _abi
+
+
+def _made_on(stream):
+    """Memory that a call makes belongs to the stream that the call uses: taken
+    from the pool of another one it could be memory whose last use there is
+    still to come."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)
 
 
 class MoELayerBuffers:
@@ -73,10 +86,10 @@ class MoELayerBuffers:
     def route_locality(self, topk_ids=None, stream=None):
         """(overlap_prev [T], [block_unique for B = 1..5]) as device tensors."""
         if not hasattr(self, "overlap_prev"):
-            dev = self.topk_ids.device
-            self.overlap_prev = torch.empty(self.T, dtype=torch.int32, device=dev)
-            self.block_unique = torch.empty(max(_abi.moe_route_locality_blocks(self.T), 1),
-                                            dtype=torch.int32, device=dev)
+            with _made_on(stream):
+                made = [torch.empty(n, dtype=torch.int32, device=self.topk_ids.device)
+                        for n in (self.T, max(_abi.moe_route_locality_blocks(self.T), 1))]
+            self.overlap_prev, self.block_unique = made
         _abi.moe_route_locality(self.shape, self.topk_ids if topk_ids is None else topk_ids,
                                 self.overlap_prev, self.block_unique, stream)
         parts, o = [], 0
@@ -155,7 +168,7 @@ class MoELayerBuffers:
         """moe_route_backward of this buffer's topk_ids and topk_w."""
         return _abi.moe_route_backward(self.shape, self.topk_ids, self.topk_w, dw, dlogits, stream)
 
-    def _train(self, kept=None):
+    def _train(self, kept=None, stream=None):
         """Memory for training, made once and kept as long as the buffer (work
         that is queued or captured in a graph may hold its addresses): the
         workspace, and a set of g and u for each form that was asked for ('act',
@@ -164,7 +177,8 @@ class MoELayerBuffers:
         dev = self.topk_ids.device
         if not hasattr(self, "train_ws"):
             n = _abi.moe_train_workspace_size(self.shape)
-            self.train_ws, self.train_ws_bytes = torch.empty(max(n, 1), dtype=torch.uint8, device=dev), n
+            with _made_on(stream):
+                self.train_ws, self.train_ws_bytes = torch.empty(max(n, 1), dtype=torch.uint8, device=dev), n
             self._kept_sets = {}
         if kept is None:
             return
@@ -173,9 +187,10 @@ class MoELayerBuffers:
         if kept not in self._kept_sets:
             P, q8 = self.T * self.k, kept == "8bit"
             dt = torch.int8 if q8 else self.y.dtype
-            g, u = (torch.empty((P, self.I), dtype=dt, device=dev) for _ in range(2))
-            gs, us = (torch.empty((P, self.I // 32), dtype=torch.uint8, device=dev) if q8 else None
-                      for _ in range(2))
+            with _made_on(stream):
+                g, u = (torch.empty((P, self.I), dtype=dt, device=dev) for _ in range(2))
+                gs, us = (torch.empty((P, self.I // 32), dtype=torch.uint8, device=dev) if q8 else None
+                          for _ in range(2))
             self._kept_sets[kept] = (g, u, gs, us, _abi.make_saved(g, u, gs, us))
         self.kept = kept
         self.g, self.u, self.g_scale, self.u_scale, self.saved = self._kept_sets[kept]
@@ -185,7 +200,7 @@ class MoELayerBuffers:
         the activation type or in 8 bits).  Each form has memory of its own,
         which stays; ffn_backward reads that of the last call of this method
         (the replay of a graph is none)."""
-        self._train(kept)
+        self._train(kept, stream)
         return _abi.moe_ffn_gate_up_save(self.shape, x, experts, self.perm if perm is None else perm,
                                          self.saved, self.h if h is None else h, self.train_ws,
                                          self.train_ws_bytes, stream)
@@ -193,7 +208,7 @@ class MoELayerBuffers:
     def ffn_backward(self, dy, x, experts, drows=None, dexperts=None, x_scale=None, perm=None,
                      stream=None):
         """moe_ffn_backward from this buffer's saved."""
-        self._train()
+        self._train(stream=stream)
         return _abi.moe_ffn_backward(self.shape, dy, x, x_scale, self.saved, experts,
                                      self.perm if perm is None else perm, drows, dexperts,
                                      self.train_ws, self.train_ws_bytes, stream)
@@ -201,7 +216,7 @@ class MoELayerBuffers:
     def router_backward(self, dw, x, w_router, dx=None, dw_router=None, dbias=None, dx_in=None,
                         stream=None):
         """moe_router_backward of this buffer's topk_ids, topk_w and perm."""
-        self._train()
+        self._train(stream=stream)
         return _abi.moe_router_backward(self.shape, self.topk_ids, self.topk_w, dw, x, w_router,
                                         self.perm, dx_in, dx, dw_router, dbias, self.train_ws,
                                         self.train_ws_bytes, stream)
@@ -225,13 +240,15 @@ class MoELayerBuffers:
         dbias and dexperts (a moe_experts of the weights' gradients), each of
         the last three only if given.  x may be its 8-bit checkpoint
         (x_scale)."""
-        self._train()
+        self._train(stream=stream)
         if not hasattr(self, "dy"):
-            made = [torch.empty_like(t) for t in (self.y, self.y, self.topk_w, self.out)]
+            with _made_on(stream):
+                made = [torch.empty_like(t) for t in (self.y, self.y, self.topk_w, self.out)]
             self.dy, self.drows, self.dw, self.dx_rows = made
         if x_scale is not None:
             if not hasattr(self, "x_back"):
-                self.x_back = torch.empty_like(self.out)
+                with _made_on(stream):
+                    self.x_back = torch.empty_like(self.out)
             _abi.moe_restore8(self.act, self.T, self.H, x, x_scale, self.x_back, stream)
             x = self.x_back
         self.combine_backward(dout, self.dy, self.dw, stream=stream)
