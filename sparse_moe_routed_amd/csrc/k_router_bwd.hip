@@ -10,15 +10,19 @@
 
 namespace moe {
 
-// w . dw of a token's slots, and dl of one of them
+// Up to here every thread takes the dot product w . dw of a token's slots itself,
+// where one launch makes all outputs and where two do: the order of the sum is the
+// same, whatever outputs are asked for.
+constexpr int kOwnDot = 16;
+
+// w . dw of a token's slots
 __device__ __forceinline__ float slots_dot(const RouterBwd& a, size_t p0, int k) {
   float dot = 0.f;
   for (int j = 0; j < k; ++j) dot = fmaf(a.w[p0 + j], a.dw[p0 + j], dot);
   return dot;
 }
 
-// One workgroup per token: dl of its pairs, then dx.  JOINT: every thread takes the
-// dot product itself, and dl is not kept.
+// One workgroup per token: dl of its pairs, then dx.  JOINT: dl is not kept.
 template <class A, bool JOINT>
 __device__ __forceinline__ void dx_token(const RouterBwd& a, int H, int E, int k, int block) {
   typedef typename A::T T;
@@ -28,7 +32,7 @@ __device__ __forceinline__ void dx_token(const RouterBwd& a, int H, int E, int k
   __shared__ float part[4];
   const size_t p0 = static_cast<size_t>(block) * k;
   float dot = 0.f;
-  if constexpr (JOINT) {
+  if (JOINT || k <= kOwnDot) {
     dot = slots_dot(a, p0, k);
   } else {
     for (int j = threadIdx.x; j < k; j += 256) dot = fmaf(a.w[p0 + j], a.dw[p0 + j], dot);
@@ -196,7 +200,7 @@ static hipError_t run(const moe_shape& s, const RouterBwd& a, hipStream_t st) {
   // 1500 top-4 of 128, 1280 float32, 31 MB of gathered rows: 13.1 -> 9.9); at 41 MB the
   // dot products taken again cost as much, at 210 MB a third more.
   const long long P = static_cast<long long>(s.T) * s.top_k;
-  if (P > 0 && s.top_k <= 16 && (a.dw_router || a.dbias) && P <= 512ll * s.E &&
+  if (P > 0 && s.top_k <= kOwnDot && (a.dw_router || a.dbias) && P <= 512ll * s.E &&
       P * s.H * static_cast<int>(sizeof(typename A::T)) <= 32 << 20)
     return few ? run_joint<A, 16>(s, a, st) : run_joint<A, 32>(s, a, st);
   if (s.T > 0) {
