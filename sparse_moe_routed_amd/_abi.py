@@ -208,8 +208,19 @@ def make_shape(T, H, E, I, top_k, act="bf16", wfmt="dense", flags=0) -> moe_shap
     return moe_shape(T, H, E, I, top_k, ACT.get(act, act), WFMT.get(wfmt, wfmt), flags)
 
 
+def _noted(struct, *tensors):
+    """The descriptor, with what its fields are the addresses of beside them
+    (type, elements, dense layout, GPU or -1, address), so that calls which write
+    through it can check that.  It holds addresses only, and no memory."""
+    struct.memory = tuple(None if t is None or isinstance(t, int) else
+                          (t.dtype, t.numel(), t.is_contiguous(), t.get_device() if t.is_cuda else -1, t.data_ptr())
+                          for t in tensors)
+    return struct
+
+
 def make_experts(gate, up, down, gate_scale=None, up_scale=None, down_scale=None) -> moe_experts:
-    return moe_experts(ptr(gate), ptr(up), ptr(down), ptr(gate_scale), ptr(up_scale), ptr(down_scale))
+    return _noted(moe_experts(ptr(gate), ptr(up), ptr(down), ptr(gate_scale), ptr(up_scale), ptr(down_scale)),
+                  gate, up, down)
 
 
 def make_perm(counts, offsets, sorted_pair, pair_row, active, n_active) -> moe_perm:
@@ -464,11 +475,13 @@ def moe_route_backward(shape, topk_ids, topk_w, dw, dlogits, stream=None, check=
 
 
 # ---------------------------------------------------------------------------
-# Training the routed experts, through the same binding.
+# Training the routed experts, through the same binding.  What these calls write
+# through a descriptor made by make_saved or make_experts (g, u and their scales,
+# the weights' gradients) is checked too; such memory may be larger than needed.
 # ---------------------------------------------------------------------------
 
 def make_saved(g, u, g_scale=None, u_scale=None) -> moe_saved:
-    return moe_saved(ptr(g), ptr(u), ptr(g_scale), ptr(u_scale))
+    return _noted(moe_saved(ptr(g), ptr(u), ptr(g_scale), ptr(u_scale)), g, u, g_scale, u_scale)
 
 
 def moe_train_workspace_size(shape) -> int:

@@ -6,13 +6,16 @@
 // C function in its order -- each a torch tensor, an address or None -- and
 // the stream's handle, and returns the status.  What a bare pointer cannot
 // tell is checked on tensors: type (MOE_E_DTYPE), size and dense layout
-// (MOE_E_SHAPE), memory of the current device (MOE_E_MEMORY).
+// (MOE_E_SHAPE), memory of the current device (MOE_E_MEMORY).  The same is
+// checked of memory that a call writes through a descriptor, where _abi.py has
+// noted what the descriptor was made from.
 //
 // A small call is bound by its host time.  Through ctypes, with these checks
 // in Python, norm_in of one row took 6.1 us a call and combine_norm of 8 rows
 // 8.1 us; through here 4.4 and 4.8, the launch itself being 3.6.
 #include <Python.h>
 #include <hip/hip_runtime_api.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "moe.h"
@@ -44,7 +47,26 @@ class Args {
   // None is a null pointer
   const moe_experts* experts() { return static_cast<const moe_experts*>(optional(g_experts_type)); }
   const moe_perm* perm() { return static_cast<const moe_perm*>(optional(g_perm_type)); }
-  const moe_saved* saved() { return static_cast<const moe_saved*>(optional(g_saved_type)); }
+  // g and u [P][I] in `act`, or with scales as codes
+  const moe_saved* saved(at::ScalarType act, Count elements) {
+    const moe_saved* s = static_cast<const moe_saved*>(optional(g_saved_type));
+    if (!s) return s;
+    const at::ScalarType type = s->g_scale || s->u_scale ? at::kChar : act;
+    noted(0, s->g, type, elements);
+    noted(1, s->u, type, elements);
+    noted(2, s->g_scale, at::kByte, elements / 32);
+    noted(3, s->u_scale, at::kByte, elements / 32);
+    return s;
+  }
+  // gradients of the weights, `elements` each
+  const moe_experts* gradients(at::ScalarType act, Count elements) {
+    const moe_experts* e = experts();
+    if (!e) return e;
+    noted(0, e->gate, act, elements);
+    noted(1, e->up, act, elements);
+    noted(2, e->down, act, elements);
+    return e;
+  }
 
   int64_t integer() {
     PyObject* o = next();
@@ -111,8 +133,7 @@ class Args {
       const at::Tensor& t = THPVariable_Unpack(o);
       if (!status_) status_ = check(t);
       if (t.is_cuda()) {
-        if (device_ < 0 && hipGetDevice(&device_) != hipSuccess) device_ = -1;
-        if (t.get_device() != device_) memory_ = MOE_E_MEMORY;
+        on(t.get_device());
         return status_ || memory_ ? nullptr : t.data_ptr();
       }
     } catch (const std::exception& e) {
@@ -121,6 +142,32 @@ class Args {
     }
     memory_ = MOE_E_MEMORY;
     return nullptr;
+  }
+  void on(int device) {
+    if (device_ < 0 && hipGetDevice(&device_) != hipSuccess) device_ = -1;
+    if (device != device_) memory_ = MOE_E_MEMORY;
+  }
+  // Field i, with address p, of the descriptor taken last: a note (type, elements,
+  // dense layout, GPU or -1, address) tells what it was made from.  No note, or one
+  // of another address: the field was given as an address.
+  void noted(Py_ssize_t i, const void* p, at::ScalarType type, Count count) {
+    if (PyErr_Occurred()) return;
+    static PyObject* const name = PyUnicode_InternFromString("memory");
+    PyObject* notes = PyObject_GetAttr(descriptor_, name);
+    if (!notes) return PyErr_Clear();
+    PyObject* n = PyTuple_Check(notes) && i < PyTuple_GET_SIZE(notes) ? PyTuple_GET_ITEM(notes, i) : nullptr;
+    if (n && PyTuple_Check(n) && PyTuple_GET_SIZE(n) == 5 && THPDtype_Check(PyTuple_GET_ITEM(n, 0)) &&
+        PyLong_AsVoidPtr(PyTuple_GET_ITEM(n, 4)) == p) {
+      if (!status_ && reinterpret_cast<THPDtype*>(PyTuple_GET_ITEM(n, 0))->scalar_type != type) status_ = MOE_E_DTYPE;
+      if (!status_ && (PyLong_AsLongLong(PyTuple_GET_ITEM(n, 1)) < count || PyTuple_GET_ITEM(n, 2) != Py_True))
+        status_ = MOE_E_SHAPE;
+      const long device = PyLong_AsLong(PyTuple_GET_ITEM(n, 3));
+      if (device < 0)
+        memory_ = MOE_E_MEMORY;
+      else
+        on(static_cast<int>(device));
+    }
+    Py_DECREF(notes);
   }
   const void* optional(PyTypeObject* type) {
     if (!given(0)) {
@@ -137,10 +184,12 @@ class Args {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "expected another descriptor");
       return zeros;
     }
+    descriptor_ = o;
     return view_[views_++].buf;
   }
   PyObject* const* a_;
   Py_ssize_t n_, i_ = 0;
+  PyObject* descriptor_ = nullptr;   // borrowed, set where structure() raised nothing
   Py_buffer view_[5];   // moe_ffn_backward has the most
   int views_ = 0;
   int status_ = 0, memory_ = 0, device_ = -1;
@@ -327,7 +376,7 @@ PyObject* ffn_gate_up_save(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   void* x = a.tensor(t, tokens(s));
   const moe_experts* ex = a.experts();
   const moe_perm* pm = a.perm();
-  const moe_saved* sv = a.saved();
+  const moe_saved* sv = a.saved(t, pairs(s) * s->I);
   void* h = a.tensor(t, pairs(s) * s->I);
   size_t bytes;
   void* ws = a.workspace(&bytes);
@@ -342,11 +391,11 @@ PyObject* ffn_backward(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   void* dy = a.tensor(t, pairs(s) * s->H);
   void* x = a.tensor(a.given(1) ? at::kChar : t, tokens(s));
   const uint8_t* x_scale = static_cast<uint8_t*>(a.tensor(at::kByte, tokens(s) / 32));
-  const moe_saved* sv = a.saved();
+  const moe_saved* sv = a.saved(t, pairs(s) * s->I);
   const moe_experts* ex = a.experts();
   const moe_perm* pm = a.perm();
   void* drows = a.tensor(t, pairs(s) * s->H);
-  const moe_experts* dex = a.experts();
+  const moe_experts* dex = a.gradients(t, static_cast<Count>(s->E) * s->I * s->H);
   size_t bytes;
   void* ws = a.workspace(&bytes);
   hipStream_t st = a.stream();
