@@ -3,6 +3,7 @@ of the layer runs in libmoe.so)."""
 from __future__ import annotations
 
 import contextlib
+import ctypes
 
 import torch
 
@@ -168,12 +169,27 @@ class MoELayerBuffers:
         """moe_route_backward of this buffer's topk_ids and topk_w."""
         return _abi.moe_route_backward(self.shape, self.topk_ids, self.topk_w, dw, dlogits, stream)
 
+    def _products(self, where, saved=False):
+        """Refuses, before the first step of `where`, a shape that the training's
+        products refuse (tiled or low-bit weights, sizes past their limits) and,
+        with `saved`, a gradient without anything saved."""
+        if not hasattr(self, "_products_status"):
+            # without pointers: what is wrong with the shape, else MOE_E_NULL (or nothing to do)
+            st = _abi.load().moe_ffn_gate_up_save(ctypes.byref(self.shape), *[None] * 6, 0, None)
+            self._products_status = 0 if st == 1 else st
+        if self._products_status:
+            raise _abi.MoEError(self._products_status, f"MoELayerBuffers.{where}")
+        if saved and not hasattr(self, "saved"):
+            raise _abi.MoEError(1, f"MoELayerBuffers.{where} before ffn_gate_up_save or layer_save")
+
     def _train(self, kept=None, stream=None):
         """Memory for training, made once and kept as long as the buffer (work
         that is queued or captured in a graph may hold its addresses): the
         workspace, and a set of g and u for each form that was asked for ('act',
-        or '8bit' with their scales).  Attributes change only once all memory
-        of a set is there."""
+        or '8bit' with their scales), which is returned.  Nothing is kept of a
+        set whose memory is not all there."""
+        if kept not in (None, "act", "8bit"):
+            raise ValueError(f"kept must be 'act' or '8bit', not {kept!r}")
         dev = self.topk_ids.device
         if not hasattr(self, "train_ws"):
             n = _abi.moe_train_workspace_size(self.shape)
@@ -181,9 +197,7 @@ class MoELayerBuffers:
                 self.train_ws, self.train_ws_bytes = torch.empty(max(n, 1), dtype=torch.uint8, device=dev), n
             self._kept_sets = {}
         if kept is None:
-            return
-        if kept not in ("act", "8bit"):
-            raise ValueError(f"kept must be 'act' or '8bit', not {kept!r}")
+            return None
         if kept not in self._kept_sets:
             P, q8 = self.T * self.k, kept == "8bit"
             dt = torch.int8 if q8 else self.y.dtype
@@ -192,22 +206,26 @@ class MoELayerBuffers:
                 gs, us = (torch.empty((P, self.I // 32), dtype=torch.uint8, device=dev) if q8 else None
                           for _ in range(2))
             self._kept_sets[kept] = (g, u, gs, us, _abi.make_saved(g, u, gs, us))
-        self.kept = kept
-        self.g, self.u, self.g_scale, self.u_scale, self.saved = self._kept_sets[kept]
+        return self._kept_sets[kept]
 
     def ffn_gate_up_save(self, x, experts, kept="act", perm=None, h=None, stream=None):
         """moe_ffn_gate_up_save into this buffer's h and saved (g and u, kept in
         the activation type or in 8 bits).  Each form has memory of its own,
         which stays; ffn_backward reads that of the last call of this method
         (the replay of a graph is none)."""
-        self._train(kept, stream)
-        return _abi.moe_ffn_gate_up_save(self.shape, x, experts, self.perm if perm is None else perm,
-                                         self.saved, self.h if h is None else h, self.train_ws,
-                                         self.train_ws_bytes, stream)
+        self._products("ffn_gate_up_save")
+        kept_set = self._train(kept, stream)
+        st = _abi.moe_ffn_gate_up_save(self.shape, x, experts, self.perm if perm is None else perm,
+                                       kept_set[4], self.h if h is None else h, self.train_ws,
+                                       self.train_ws_bytes, stream)
+        self.kept = kept
+        self.g, self.u, self.g_scale, self.u_scale, self.saved = kept_set
+        return st
 
     def ffn_backward(self, dy, x, experts, drows=None, dexperts=None, x_scale=None, perm=None,
                      stream=None):
         """moe_ffn_backward from this buffer's saved."""
+        self._products("ffn_backward", saved=True)
         self._train(stream=stream)
         return _abi.moe_ffn_backward(self.shape, dy, x, x_scale, self.saved, experts,
                                      self.perm if perm is None else perm, drows, dexperts,
@@ -223,11 +241,14 @@ class MoELayerBuffers:
 
     def layer_save(self, x, w_router, bias, experts, residual=None, out=None, kept="act", stream=None):
         """The whole layer, keeping in this buffer what layer_backward needs (the
-        routes, the permutation, y, g and u).  experts are dense and row-major.
-        A buffer with check_finite is refused (MOE_E_FLAGS): these steps do not
-        check."""
+        routes, the permutation, y, g and u).  experts are dense and row-major,
+        and no pair is dropped.  A buffer made tiled, fused or with check_finite
+        (these steps do not check) is refused (MOE_E_FLAGS), and one of low-bit
+        weights (MOE_E_FORMAT)."""
         if self.shape.flags & _abi.MOE_F_CHECK_FINITE:
             raise _abi.MoEError(10, "MoELayerBuffers.layer_save with check_finite")
+        self._products("layer_save")
+        self._train(kept, stream)
         self.route_permute(x, w_router, bias, logits=False, stream=stream)
         self.ffn_gate_up_save(x, experts, kept, stream=stream)
         self.ffn_down(experts, stream=stream)
@@ -240,6 +261,7 @@ class MoELayerBuffers:
         dbias and dexperts (a moe_experts of the weights' gradients), each of
         the last three only if given.  x may be its 8-bit checkpoint
         (x_scale)."""
+        self._products("layer_backward", saved=True)
         self._train(stream=stream)
         if not hasattr(self, "dy"):
             with _made_on(stream):
