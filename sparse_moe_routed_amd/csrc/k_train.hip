@@ -83,8 +83,10 @@ static hipError_t launch_tiles(const moe_shape& s, const TrainPlan& pl, const mo
 template <bool WIDE, class F>
 static hipError_t with_shape(const moe_shape& s, const RowCut& c, F&& f) {
   const bool once = static_cast<int64_t>(s.T) * s.top_k <= static_cast<int64_t>(s.E) * row_height(c.shape);
-  if constexpr (WIDE)
-    if (c.shape == kRowsWide) return f(Wide{});
+  if (c.shape == kRowsWide) {
+    if constexpr (WIDE) return f(Wide{});
+    return hipErrorInvalidValue;   // a product that is not made in this shape
+  }
   if (c.shape == kRowsFew) return once ? f(FewOnce{}) : f(Few{});
   return once ? f(ManyOnce{}) : f(Many{});
 }

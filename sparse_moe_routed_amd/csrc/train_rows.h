@@ -429,14 +429,16 @@ __device__ __forceinline__ void store_dh(const DhArgs& o, size_t at, const float
   store_vals<E>(static_cast<typename E::T*>(o.h) + at, h);
 }
 
-// dh of one tile of BM rows x BN columns.
-template <class E, class S, int OUT, bool JOIN = false>
+// dh of one tile of BM rows x BN columns.  Not in the 256 x 256 shape, whose sums
+// may be cut at the end: it is slower here.
+template <class E, class S, int OUT>
 __global__ __launch_bounds__(S::THREADS, 2) void k_dh(RowArgs a, const void* __restrict__ dy,
                                                       const void* __restrict__ wd, DhArgs o) {
+  static_assert(!S::WIDE, "no cut tiles here");
   __shared__ __align__(16) char lds[S::STAGES * S::BYTES];
   const int H = a.H, I = a.I;
   TileOf tl;
-  if (!tile_of_block<S, JOIN>(a, (I + S::BN - 1) / S::BN, H / E::BK, blockIdx.x, tl)) return;
+  if (!tile_of_block<S, false>(a, (I + S::BN - 1) / S::BN, H / E::BK, blockIdx.x, tl)) return;
   Tiles<E, S> T;
   const int col0 = tl.slab * S::BN;
   const char* down = static_cast<const char*>(wd) + (static_cast<size_t>(tl.e) * H * I + col0) * E::SZ;
@@ -448,7 +450,7 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_dh(RowArgs a, const void* __r
   T.cols(noff, krow, I * E::SZ, I - col0);
 
   const int stages = H / E::BK, s0 = tl.part * stages / tl.cut;
-  const auto products = [&] { T.run(
+  T.run(
       (tl.part + 1) * stages / tl.cut - s0, lds,
       [&](int s, char* st) {
         const u32x4_t rn = buffer(down + static_cast<size_t>(s0 + s) * E::BK * I * E::SZ);
@@ -461,14 +463,7 @@ __global__ __launch_bounds__(S::THREADS, 2) void k_dh(RowArgs a, const void* __r
       [&](const char* st, int ks, typename Tiles<E, S>::Frags& f) {
         T.read_n(st, ks, f);
         T.read_m(st, ks, f);
-      }); };
-  if constexpr (JOIN) {
-    T.add_cuts(a.part, tl.slot, tl.cut);
-  } else {
-    products();
-    if constexpr (S::WIDE)
-      if (tl.cut > 1) return T.store_cut(a.part, tl.slot);
-  }
+      });
 
 #pragma unroll
   for (int t = 0; t < S::MF; ++t) {
