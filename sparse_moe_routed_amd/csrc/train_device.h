@@ -105,27 +105,34 @@ __device__ __forceinline__ u32x4_t buffer(const void* p) {
 // Written as assembly because the compiler, which knows that such a load
 // writes LDS but not where, waits for all of them before the next transposing
 // LDS read; here the waits are stage_barrier()'s.  Nothing but LDS is written,
-// and the registers are read when the load is issued.  The five wait states in
-// front are what a buffer load needs after the vector unit has written one
-// of its scalar registers.
+// and the registers are read when the load is issued.  m0 holds the LDS address
+// and is declared as overwritten (the warning says that it is not saved, which is
+// not wanted; as an operand that the compiler writes it took 0.7% longer: 8192 x
+// 2560 x 5120 backward 1384 -> 1394 us).  The five wait states in front are what a
+// buffer load needs after the vector unit has written one of its scalar registers.
+// stage_barrier()'s counts hold only the memory operations written here: a kernel
+// must not spill vector registers.
 // ONCE: data that is read about once leaves the caches first (256 tokens, 512 experts of
 // 2560 x 640: dh 330 -> 270 us, dx 570 -> 520; where weights are read again, at
 // 8192 rows of one expert, it costs: 335 -> 356).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <bool ONCE = false>
 __device__ __forceinline__ void load_lds(u32x4_t rs, char* lds, uint32_t off) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS char*)lds)));
   if constexpr (ONCE)
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds"
-                 ::"v"(off), "s"(rs), "s"(at) : "memory");
+                 ::"v"(off), "s"(rs), "s"(at) : "memory", "m0");
   else
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                 ::"v"(off), "s"(rs), "s"(at) : "memory");
+                 ::"v"(off), "s"(rs), "s"(at) : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds_word(u32x4_t rs, char* lds, uint32_t off) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS char*)lds)));
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dword %0, %1, 0 offen lds"
-               ::"v"(off), "s"(rs), "s"(at) : "memory");
+               ::"v"(off), "s"(rs), "s"(at) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Rows of expert e within [0, P), whatever the offsets hold.
 __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int P, int& row0, int& rows) {
