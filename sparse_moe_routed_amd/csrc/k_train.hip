@@ -78,11 +78,10 @@ static hipError_t launch_tiles(const moe_shape& s, const TrainPlan& pl, const mo
   return hipGetLastError();
 }
 
-// f(shape) of a cut.  Where an expert's rows are about one tile, a weight is read
-// about once.
+// f(shape) of a cut.
 template <bool WIDE, class F>
 static hipError_t with_shape(const moe_shape& s, const RowCut& c, F&& f) {
-  const bool once = static_cast<int64_t>(s.T) * s.top_k <= static_cast<int64_t>(s.E) * row_height(c.shape);
+  const bool once = read_once(s, c);
   if (c.shape == kRowsWide) {
     if constexpr (WIDE) return f(Wide{});
     return hipErrorInvalidValue;   // a product that is not made in this shape
@@ -108,9 +107,6 @@ hipError_t launch_gate_up_save(const moe_shape& s, const TrainPlan& pl, const vo
                               : gate_up<TF32>(s, pl, x, ex, pm, sv, h, ws, st);
 }
 
-// Most workgroups of the rows' gradient that share the weight gradients' launch.
-constexpr int kJointBlocks = 512;
-
 template <class E>
 static hipError_t rows_backward(const moe_shape& s, const TrainPlan& pl, const void* dy, const DhArgs& d,
                                 const moe_experts& ex, const moe_perm& pm, void* drows, void* ws, hipStream_t st) {
@@ -121,11 +117,10 @@ static hipError_t rows_backward(const moe_shape& s, const TrainPlan& pl, const v
   return with_shape<true>(s, pl.dx, [&](auto shape) { return run_dx<E, decltype(shape)>(b, d, ex, drows, st); });
 }
 
-hipError_t launch_ffn_backward(const moe_shape& s, const TrainPlan& plan, const void* dy,
+hipError_t launch_ffn_backward(const moe_shape& s, const TrainPlan& pl, const void* dy,
                                const void* x, const uint8_t* x_scale, const moe_saved* sv,
                                const moe_experts& ex, const moe_perm* pm, void* drows,
                                const moe_experts* dex, void* ws, hipStream_t st) {
-  TrainPlan pl = plan;
   const bool bf16 = s.act == MOE_DT_BF16;
   DwArgs a{};
   DxArgs dx{};
@@ -135,9 +130,6 @@ hipError_t launch_ffn_backward(const moe_shape& s, const TrainPlan& plan, const 
   a.I = s.I;
   a.P = s.T * s.top_k;
   if (a.P > 0) {
-    // one list of short tiles serves both products
-    if (s.E > kLookupExperts && pl.dx.shape == kRowsFew && pl.dh.shape == kRowsMany) pl.dx.shape = kRowsMany;
-    if (s.E > kLookupExperts && pl.dx.shape == kRowsMany && pl.dh.shape == kRowsFew) pl.dh.shape = kRowsMany;
     const bool wide = drows && pl.dx.shape == kRowsWide;
     hipError_t e = launch_tiles(s, pl, *pm, ws, row_height(pl.dh.shape), wide, st);
     if (e == hipSuccess && dex && x_scale) {
@@ -147,16 +139,15 @@ hipError_t launch_ffn_backward(const moe_shape& s, const TrainPlan& plan, const 
     }
     const DhArgs d{sv->g, sv->u, sv->g_scale, sv->u_scale, at_off<char>(ws, pl.dg_off), at_off<char>(ws, pl.du_off),
                    at_off<char>(ws, pl.h_off)};
-    joint = drows && dex && pl.dx.shape == kRowsFew && pl.dx.parts == 1 && pl.dw_parts == 1;
+    joint = drows && dex && pl.joint;
     if (joint) {
       dx.rows = row_args(s, pl, *pm, ws, pl.dx);
       dx.gate = ex.gate;
       dx.up = ex.up;
       dx.drows = drows;
       dx.blocks = tile_grid<Few>(dx.rows, s.H / 128);
-      joint = dx.blocks <= kJointBlocks;
+      drows = nullptr;
     }
-    if (joint) drows = nullptr;
     if (e == hipSuccess)
       e = bf16 ? rows_backward<TBf16>(s, pl, dy, d, ex, *pm, drows, ws, st)
                : rows_backward<TF32>(s, pl, dy, d, ex, *pm, drows, ws, st);

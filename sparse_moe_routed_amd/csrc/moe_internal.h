@@ -201,6 +201,7 @@ struct RowCut {
 };
 constexpr int row_height(int shape) { return shape == kRowsFew ? 32 : shape == kRowsMany ? 128 : 256; }
 constexpr int kLookupExperts = 64;   // up to here a wave finds its tile itself
+constexpr int kJointBlocks = 512;    // most workgroups of the rows' gradient that share the weight gradients' launch
 #ifdef __HIPCC__
 #define MOE_BOTH __host__ __device__ inline
 #else
@@ -250,6 +251,7 @@ struct Tail {
 struct TrainPlan {
   RowCut gate_up, dh, dx;
   int dw_parts;   // parts of an expert's rows in the weight gradients, 0: by 256 x 256 tiles
+  bool joint;     // the rows' and the weights' gradients, where both are wanted, are one launch
   // tile lists, by row height 32 or 128 / 256: int32 [3 * most] (expert, row0, rows), then their number
   int most[2];
   size_t tiles_off[2];
@@ -261,6 +263,8 @@ struct TrainPlan {
   size_t total;
 };
 void make_train_plan(const moe_shape& s, TrainPlan* p);
+// Whether an expert's rows are about one tile, so that a weight is read about once.
+bool read_once(const moe_shape& s, const RowCut& c);
 bool train_fits(const moe_shape& s, const TrainPlan& p);   // the limits of the two products
 
 hipError_t launch_save8(bool f32, size_t n, const void* v, int8_t* codes, uint8_t* scales,

@@ -100,6 +100,11 @@ void make_train_plan(const moe_shape& s, TrainPlan* p) {
   // (8192 x 2560 x 5120: 330 us at 128 rows, 384 at 256)
   p->dh = best_cut(s, s.I, s.H, false, false);
   p->dx = best_cut(s, s.H, 2 * s.I, false, true);
+  // one list of short tiles serves both products of the gradient
+  if (s.E > kLookupExperts && p->dx.shape == kRowsFew && p->dh.shape == kRowsMany) p->dx.shape = kRowsMany;
+  if (s.E > kLookupExperts && p->dx.shape == kRowsMany && p->dh.shape == kRowsFew) p->dh.shape = kRowsMany;
+  const size_t blocks = (P / row_height(kRowsFew) + std::min<size_t>(s.E, P)) * (s.H / 128);
+  p->joint = p->dx.shape == kRowsFew && p->dx.parts == 1 && p->dw_parts == 1 && (blocks + 7) / 8 * 8 <= kJointBlocks;
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     const size_t off = at;
@@ -125,6 +130,10 @@ void make_train_plan(const moe_shape& s, TrainPlan* p) {
   at = 0;
   p->dl_off = take(P * 4);
   p->total = std::max(products, at);
+}
+
+bool read_once(const moe_shape& s, const RowCut& c) {
+  return static_cast<int64_t>(s.T) * s.top_k <= static_cast<int64_t>(s.E) * row_height(c.shape);
 }
 
 bool train_fits(const moe_shape& s, const TrainPlan& p) {
