@@ -580,9 +580,12 @@ int moe_route_backward(const moe_shape* shape, const int32_t* topk_ids, const fl
  * largest magnitude of the 32 (at most 248, where codes past 127 are cut to
  * 127, so that no finite number reads back as infinity), and codes rounded to
  * nearest even.  A power of two makes every kept value exact in bf16 and the
- * codes independent of how the scale is applied; the rounding error is at
- * most half a unit of the code, 1/127 of the largest magnitude.  32 elements
- * among which is a NaN or an infinity have scale 255 and read back as NaN. */
+ * codes independent of how the scale is applied.  The error is at most half a
+ * unit 2^(scale-127) of the code, or less than one where a code of scale 248 is
+ * cut (float32 only: bf16 ends at 127.5 units); from scale 2 on that is at most
+ * 1/127 of the largest magnitude, at scale 1 it is 2^-127, whatever the
+ * magnitudes.  32 elements among which is a NaN or an infinity have scale 255
+ * and read back as NaN. */
 
 /* What the gated product keeps for its gradient: g and u [P][I], in the act
  * type (both scale pointers NULL) or as 8-bit checkpoints (codes, and the
