@@ -53,6 +53,8 @@ struct TBf16 {
   static __device__ __forceinline__ void mma32(u32x4_t n, u32x4_t m, f32x16_t& c) {
     asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(n), "v"(m));
   }
+  // exp2 of a rounded product: off by |g| 2^-24 of the value and a few 2^-24, far
+  // below the half step 2^-8 of what is made from it
   static __device__ __forceinline__ float exp_neg(float g) { return __expf(-g); }
 };
 
@@ -310,7 +312,8 @@ __device__ __forceinline__ void line_pieces(const f32x4_t (&a)[4], int lane, F&&
   }
 }
 
-// Division by the number of slots: p / k = (t + ((p - t) >> 1)) >> s with t = high word of
+// Division by the number of slots (by the round-up method of Granlund and
+// Montgomery, "Division by invariant integers using multiplication", 1994): p / k = (t + ((p - t) >> 1)) >> s with t = high word of
 // p m, m = floor(2^32 (2^(s + 1) - k) / k) + 1, 2^s < k <= 2^(s + 1), for any 32-bit p.
 struct PairDiv {
   uint32_t k, m, s;

@@ -6,12 +6,18 @@
 // Weights are read as they lie in memory: the transposing LDS read serves the
 // sides whose sum index is not contiguous (train_device.h).
 //
-// What bounds them.  Experts of few rows: the weights' bytes (512 experts of 2560 x
-// 640, bf16: 256 tokens top-10 k_dh 267 us, 6.3 TB/s, k_dx 520 us, 6.5; 4096 tokens
-// k_gate_up_save 772, k_dh 465, k_dx 795, 4.3 to 4.9 TB/s with 80 of a tile's 128
-// rows filled).  One expert of many rows: the matrix cores (8192 rows of 2560 x 5120:
-// k_gate_up_save 395 us, 1090 TFLOP/s, k_dh 326 us with its activations, k_dx 389 +
-// 19).  A handful of tiles: the latency of one tile, 7 to 10 us.
+// What bounds them (the fastest of 12 runs, which is what long rows of calls take too;
+// the 5th to 25th call from idle take up to a third more, as a library's products
+// do).  Experts of few rows: the weights' bytes (512 experts of 2560 x 640, bf16: 256
+// tokens top-10 k_dh 267 us, 6.3 TB/s, k_dx 520 us, 6.5; 4096 tokens k_gate_up_save 760
+// to 770, k_dh 465, k_dx 795, 4.3 to 4.9 TB/s with 80 of a tile's 128 rows filled).
+// One expert of many rows: the matrix cores (8192 rows of 2560 x 5120: k_gate_up_save
+// 395 us, 1090 TFLOP/s, k_dh 326 us with its activations, k_dx 389 + 19).  A handful
+// of tiles: the latency of one tile, 7 to 10 us.  One block of tens to hundreds of
+// rows: its launches, as a sum that is split is joined by another one (gradient of 53
+// rows 3456 x 928 bf16 35 us, of 38 rows 2816 x 1152 float32 60).  Float32 of many rows:
+// the matrix cores, on tiles that are filled in part (404 rows an expert in four
+// tiles of 128; 640 columns in three slabs of 256).
 #pragma once
 
 #include <type_traits>

@@ -260,7 +260,9 @@ class MoELayerBuffers:
         (plus dx_in, for instance dout where the residual was x), dw_router,
         dbias and dexperts (a moe_experts of the weights' gradients), each of
         the last three only if given.  x may be its 8-bit checkpoint
-        (x_scale)."""
+        (x_scale).  dx is rounded to the activation type twice: what comes
+        through the experts with dx_in, and that with what comes through the
+        router."""
         self._products("layer_backward", saved=True)
         self._train(stream=stream)
         if not hasattr(self, "dy"):
