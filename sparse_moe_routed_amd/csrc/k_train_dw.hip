@@ -19,11 +19,11 @@ namespace moe {
 // the steps of all tiles are one pipeline, so the next loads are on their way
 // while a tile is stored.  PART: float32 sums of a part of the rows.
 //
-// Bound by the stores (fastest of 12 runs; medians 985 and 1250): 512 experts of 2560 x 640 are 5.0 GB of gradients, at five
-// rows each 920 us, at 80 skewed ones 1250 (there reads of x, dy and h that miss
-// L2, 1.35 GB, compete with them).  Stores of whole cache lines that leave the
-// caches first took 1600 us to 1290, steps of half a stage seven deep the five rows
-// from 1100 to 1010.
+// Bound by the stores: 512 experts of 2560 x 640 are 5.0 GB of gradients, at five
+// rows each 920 to 940 us, at 80 skewed ones 1200 (there reads of x, dy and h that
+// miss L2, 1.35 GB, compete with them; the fastest of 12 runs, the medians are 985
+// and 1250).  Stores of whole cache lines that leave the caches first took 1600 us to
+// 1290, steps of half a stage seven deep the five rows from 1100 to 1010.
 template <class E, bool PART>
 struct DwStrip {
   typedef Shape<2, 2, 4, 2, 16> S;
