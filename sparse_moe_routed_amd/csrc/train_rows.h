@@ -427,7 +427,12 @@ __device__ __forceinline__ void store_dh(const DhArgs& o, size_t at, const float
     const float sig = 1.0f / (1.0f + E::exp_neg(g[j])), gs = g[j] * sig;
     h[j] = gs * u[j];
     const float du = dh[j] * gs;
-    g[j] = dh[j] * u[j] * sig * (1.0f + g[j] * (1.0f - sig));   // dg
+    // dg: the slope, at most 1.1, goes to the larger factor first, so that no product on
+    // the way leaves float32's range where the result does not (dh u = 1e42 behind a
+    // gate of -60)
+    const float slope = sig * (1.0f + g[j] * (1.0f - sig));
+    const bool first = fabsf(dh[j]) >= fabsf(u[j]);
+    g[j] = (first ? dh[j] : u[j]) * slope * (first ? u[j] : dh[j]);
     u[j] = du;
   }
   store_vals<E>(static_cast<typename E::T*>(o.dg) + at, g);
