@@ -210,11 +210,14 @@ def make_shape(T, H, E, I, top_k, act="bf16", wfmt="dense", flags=0) -> moe_shap
 
 def _noted(struct, *tensors):
     """The descriptor, with what its fields are the addresses of beside them
-    (type, elements, dense layout, GPU or -1, address), so that calls which write
-    through it can check that.  It holds addresses only, and no memory."""
-    struct.memory = tuple(None if t is None or isinstance(t, int) else
-                          (t.dtype, t.numel(), t.is_contiguous(), t.get_device() if t.is_cuda else -1, t.data_ptr())
-                          for t in tensors)
+    (type, elements, dense layout, GPU, address), so that calls which write
+    through it can check that.  It holds addresses only, and no memory.  The GPU
+    is None for pinned host memory, which every one can write, and -1 for other
+    host memory."""
+    struct.memory = tuple(
+        None if t is None or isinstance(t, int) else
+        (t.dtype, t.numel(), t.is_contiguous(),
+         t.get_device() if t.is_cuda else None if t.is_pinned() else -1, t.data_ptr()) for t in tensors)
     return struct
 
 

@@ -148,8 +148,9 @@ class Args {
     if (device != device_) memory_ = MOE_E_MEMORY;
   }
   // Field i, with address p, of the descriptor taken last: a note (type, elements,
-  // dense layout, GPU or -1, address) tells what it was made from.  No note, or one
-  // of another address: the field was given as an address.
+  // dense layout, GPU, address) tells what it was made from; no GPU: pinned host
+  // memory, -1: other host memory.  No note, or one of another address: the field was
+  // given as an address.
   void noted(Py_ssize_t i, const void* p, at::ScalarType type, Count count) {
     if (PyErr_Occurred()) return;
     static PyObject* const name = PyUnicode_InternFromString("memory");
@@ -161,11 +162,13 @@ class Args {
       if (!status_ && reinterpret_cast<THPDtype*>(PyTuple_GET_ITEM(n, 0))->scalar_type != type) status_ = MOE_E_DTYPE;
       if (!status_ && (PyLong_AsLongLong(PyTuple_GET_ITEM(n, 1)) < count || PyTuple_GET_ITEM(n, 2) != Py_True))
         status_ = MOE_E_SHAPE;
-      const long device = PyLong_AsLong(PyTuple_GET_ITEM(n, 3));
-      if (device < 0)
-        memory_ = MOE_E_MEMORY;
-      else
-        on(static_cast<int>(device));
+      if (PyTuple_GET_ITEM(n, 3) != Py_None) {
+        const long device = PyLong_AsLong(PyTuple_GET_ITEM(n, 3));
+        if (device < 0)
+          memory_ = MOE_E_MEMORY;
+        else
+          on(static_cast<int>(device));
+      }
     }
     Py_DECREF(notes);
   }

@@ -126,3 +126,30 @@ def test_on_the_gpu():
     assert calls(M.make_saved(*keep), M.make_experts(dw[0], dw[1], dw[2].mT)) == (0, SHAPE)
     assert calls(M.make_saved(*keep), M.make_experts(dw[0].cpu(), dw[1], dw[2])) == (0, MEMORY)
     torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_pinned_host_memory():
+    """g, u and a gradient in pinned host memory, which the GPU writes: the values of
+    the same call with memory of the GPU."""
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev).manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, device=dev).bfloat16()
+    shape = M.make_shape(T, H, E, I, K)
+    offsets = torch.arange(E + 1, dtype=torch.int32, device=dev)
+    pair = torch.arange(P, dtype=torch.int32, device=dev)
+    perm = M.make_perm(None, offsets, pair, None, None, None)
+    ws = torch.empty(M.moe_train_workspace_size(shape), dtype=U8, device=dev)
+    w, x, dy = [r(E, I, H), r(E, I, H), r(E, H, I)], r(T, H), r(P, H)
+    h, drows = torch.empty(P, I, dtype=BF, device=dev), torch.empty(P, H, dtype=BF, device=dev)
+    got = []
+    for where in (dict(device=dev), dict(pin_memory=True)):
+        keep = [torch.empty(P, I, dtype=BF, **where) for _ in range(2)]
+        dw = [torch.empty(s, dtype=BF, **where) for s in ((E, I, H), (E, I, H), (E, H, I))]
+        saved = M.make_saved(*keep)
+        M.moe_ffn_gate_up_save(shape, x, M.make_experts(*w), perm, saved, h, ws, ws.numel())
+        M.moe_ffn_backward(shape, dy, x, None, saved, M.make_experts(*w), perm, drows, M.make_experts(*dw), ws,
+                           ws.numel())
+        torch.cuda.synchronize()
+        got.append([t.cpu() for t in (*keep, *dw, drows)])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
