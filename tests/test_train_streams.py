@@ -108,3 +108,58 @@ def test_memory_comes_from_the_streams_pool(as_handle):
     # all of it is free now, in the current stream's pool
     side = torch.cuda.Stream()
     assert owners(run(side.cuda_stream if as_handle else side)) == {side.cuda_stream}
+
+
+@pytest.mark.gpu
+def test_the_default_streams_handle():
+    """A handle of 0 is the default stream."""
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev).manual_seed(2)
+    r = lambda *s: (torch.randn(*s, generator=g, device=dev) * 0.1).bfloat16()
+    x, wr, w = r(T, H), r(E, H), [r(E, I, H), r(E, I, H), r(E, H, I)]
+    got = []
+    for stream in (None, 0, torch.cuda.default_stream()):
+        buf, dx = M.MoELayerBuffers(T, H, E, I, K, device=dev), torch.empty_like(x)
+        buf.layer_save(x, wr, None, M.make_experts(*w), stream=stream)
+        buf.layer_backward(x, x, wr, M.make_experts(*w), dx, stream=stream)
+        torch.cuda.synchronize()
+        got.append((buf.out, dx))
+    assert all(torch.equal(a, b) for other in got[1:] for a, b in zip(got[0], other))
+
+
+@pytest.mark.gpu
+def test_memory_made_while_a_graph_is_captured():
+    """The first step of a buffer may be a captured one: replays and eager steps between
+    them agree, with memory freed and taken again in between."""
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev).manual_seed(4)
+    r = lambda *s: (torch.randn(*s, generator=g, device=dev) * 0.1).bfloat16()
+    T, H, E, I, K = 70, 256, 6, 96, 2
+    x, wr, w = r(T, H), r(E, H), [r(E, I, H), r(E, I, H), r(E, H, I)]
+    dx, dw = torch.empty_like(x), [torch.empty_like(t) for t in w]
+    ex, dex = M.make_experts(*w), M.make_experts(*dw)
+
+    def step(buf, kept):
+        buf.layer_save(x, wr, None, ex, kept=kept)
+        buf.layer_backward(x, x, wr, ex, dx, dexperts=dex)
+
+    want = {}
+    for kept in ("act", "8bit"):
+        other = M.MoELayerBuffers(T, H, E, I, K, device=dev)
+        step(other, kept)
+        torch.cuda.synchronize()
+        want[kept] = [t.clone() for t in (other.out, dx, *dw)]
+    buf, graphs = M.MoELayerBuffers(T, H, E, I, K, device=dev), {}
+    for kept in ("act", "8bit"):
+        graphs[kept] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[kept]):
+            step(buf, kept)
+    for _ in range(3):
+        for kept in ("8bit", "act"):
+            for run in (graphs[kept].replay, lambda: step(buf, kept), graphs[kept].replay):
+                for t in (buf.out, dx, *dw):
+                    t.fill_(7)
+                torch.full((1 << 20,), 3.0, device=dev)            # taken and given back
+                run()
+                torch.cuda.synchronize()
+                assert all(torch.equal(a, b) for a, b in zip((buf.out, dx, *dw), want[kept])), kept
